@@ -47,7 +47,7 @@ NOMINAL_HBM_GBS = 8000.0            # the roofline the target is stated against
 FALLBACK_HBM_GBS = 6800.0           # used only when MEASURED_PEAKS.json is absent
 # DRAM bytes (read + write) per launch of the scoring kernel on the default
 # workload, from one ncu capture of this kernel code (identified by its hash).
-NCU_TRAFFIC = {"source_sha1": "5cb170908f66cd1a695bef1deab314f034cf2fef",
+NCU_TRAFFIC = {"source_sha1": "3971cc069722643e49901b3e3ad1dbfe1ae659bc",
                "bytes_per_launch": 29925604608 + 7847680, "config": 3}
 GENERAL_TAU = 0.3                   # a temperature whose 1/tau is not 1, 2, 4 or 8
 
@@ -94,12 +94,12 @@ def peaks():
 
 
 def kernel_source_sha1() -> str:
-    """Hash of the scoring kernel's code (its two source files with comments,
+    """Hash of the scoring kernel's code (its source files with comments,
     blank lines and trailing blanks removed): the ncu traffic below is
     reported only while the code it was captured from is unchanged."""
     import re
     h = hashlib.sha1()
-    for name in ("ps_score_rows.cu", "ps_internal.cuh"):
+    for name in ("ps_score_rows.cu", "ps_row_sums.cuh", "ps_internal.cuh"):
         with open(os.path.join(ROOT, "mh_prefetch_subtree_gb300", "csrc", name)) as f:
             src = f.read()
         src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)

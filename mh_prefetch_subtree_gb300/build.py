@@ -50,7 +50,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 def _build_locked(force: bool, verbose: bool) -> str:
-    headers = [os.path.join(CSRC, "ps_internal.cuh"), os.path.join(ROOT, "include", "ps.h")]
+    headers = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith(".cuh")]
+    headers.append(os.path.join(ROOT, "include", "ps.h"))
     procs, objs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)
