@@ -82,6 +82,7 @@ typedef enum { PS_BF16 = 0, PS_F32 = 1 } ps_dtype;
 #define PS_DEV_TIMEOUT       0x20  /* a bounded wait on a bulk copy gave up */
 #define PS_DEV_BAD_ROW_INDEX 0x40  /* row_index outside [0, n_logit_rows) */
 #define PS_DEV_BAD_UNIFORM   0x80  /* walk: an acceptance uniform outside (0, 1] */
+#define PS_DEV_BAD_RULES     0x100 /* rules: a sequence, length, mask or bias entry, or a parameter */
 
 /* Request codes of a tree node's `req` entry. */
 #define PS_NODE_LEAF     (-1)     /* not expanded: the walk stops here */
@@ -491,6 +492,139 @@ ps_status ps_selftest_wait_timeout(uint64_t limit_ns, int32_t *status, void *cud
  *         loads.
  */
 ps_status ps_selftest_read(const void *data, size_t bytes, uint32_t *sink, void *cuda_stream);
+
+/*
+ * Rules on logits rows: penalties for repeated tokens, biases and grammar
+ * masks.  A sampler that decodes its proposals under such rules has to score
+ * them under the same rules, or the log q terms of eq. (6) are those of another
+ * proposal.  (The PreSTO pages decode without rules: Appendix D.3 takes
+ * log_softmax(logits / tau), Table 6 lists none.)
+ *
+ * Row r belongs to sequence s = row_seq[r] and sees its first n = row_len[r]
+ * tokens.  With c_v the number of times id v is among the sequence's tokens
+ * seq_prompt[s] .. n-1 (the generated ones) and "seen" meaning among tokens
+ * 0 .. n-1, the processed logit of id v is
+ *     l'_v = -inf                                        if the row's mask bit v is 0,
+ *     l'_v = p_v - frequency c_v - presence [c_v > 0] + bias_v      otherwise,
+ *     p_v  = l_v / repetition if l_v > 0, else l_v repetition, if v was seen;  l_v if not.
+ * The arithmetic is float32, and a bfloat16 result is rounded once.  An id that
+ * no rule touches keeps its logit bit for bit.  A masked id is -inf whatever
+ * its logit holds, NaN included.
+ *
+ * n_seqs        number of sequences, >= 0.
+ * seq_begin     [n_seqs+1] CSR offsets into seq_tokens, or NULL: no history, so
+ *               no penalties (the five arrays down to presence are then not read).
+ * seq_tokens    [n_tokens] int32 ids.
+ * seq_prompt    [n_seqs] or NULL (0): leading tokens that are the prompt, which
+ *               count as seen and not as generated.
+ * repetition    [n_seqs] float32, > 0, or NULL (1).
+ * frequency, presence   [n_seqs] float32 or NULL (0).
+ * bias_begin    [n_seqs+1] CSR offsets into bias_ids and bias_values, or NULL:
+ *               no biases.  The ids of one sequence rise strictly.
+ * mask          [n_masks][mask_ld] 32-bit words, or NULL: no masks.  Bit v % 32
+ *               of word v / 32 is 1 where id v is allowed; mask_ld >= ceil(V/32).
+ *               Bits from V on are ignored.
+ * row_seq       [n_rows], or NULL: row r belongs to sequence r.
+ * row_len       [n_rows], or NULL: a row sees its whole sequence.
+ * row_mask      [n_rows]: the row's mask, or -1 for none; NULL: row r has mask r.
+ *
+ * What only the device can see sets bits in the status word, and the row's
+ * results are NaN: PS_DEV_BAD_TOKEN for a history token outside [0, V);
+ * PS_DEV_BAD_RULES for row_seq, row_len, row_mask, seq_begin or bias_begin out of
+ * range, a bias id outside [0, V) or not above the one before it, or a penalty
+ * that is not finite (repetition: not > 0).
+ */
+typedef struct {
+    int32_t n_seqs;
+    int32_t n_masks;
+    int64_t n_tokens;
+    int64_t n_bias;
+    int64_t mask_ld;
+    const int64_t *seq_begin;
+    const int32_t *seq_tokens;
+    const int32_t *seq_prompt;
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const int64_t *bias_begin;
+    const int32_t *bias_ids;
+    const float *bias_values;
+    const uint32_t *mask;
+    const int32_t *row_seq;
+    const int32_t *row_len;
+    const int32_t *row_mask;
+} ps_logit_rules;
+
+/*
+ * Processed rows: out[r] = the rules applied to logits[r], for decoding.
+ *
+ * logits     [n_rows][ld], dtype, laid out as in ps_subtree_batch (16-byte
+ *            aligned rows, at most 2^30 bytes each).
+ * out        [n_rows][out_ld] of the same dtype, 16-byte aligned rows.  It is
+ *            either apart from logits or the same array with out_ld == ld (in
+ *            place); a partial overlap gives PS_ERR_INVALID_ARG.  Elements
+ *            V..out_ld-1 of a row are not written.
+ * status     device int32 word, required; the caller zeroes it.
+ * n_rows == 0 does nothing.
+ */
+ps_status ps_process_rows(const ps_logit_rules *rules, int32_t V, int32_t dtype, int64_t n_rows,
+                          const void *logits, int64_t ld, void *out, int64_t out_ld,
+                          int32_t *status, void *cuda_stream);
+
+/*
+ * log p0 and log q_tau of every row's token under rules: ps_score_rows of the
+ * rows that ps_process_rows would write in float32, without writing them.  p0 is
+ * softmax(l') and q_tau softmax(l' / tau).  The batch is read as by ps_score_rows
+ * (rules are indexed by the scored row r, logits by row_index[r] when given).
+ * lp0, lq, entropy, status: as for ps_score_rows.  A token that the row's mask
+ * forbids has log-probability -inf.  A row with no finite logit left (a mask
+ * that allows nothing, say) gives NaN and PS_DEV_NONFINITE, as in
+ * ps_score_rows; logits in masked places are not looked at.
+ * workspace  device memory, 256-byte aligned, >= ps_rules_workspace_bytes(batch):
+ *            partial sums of every row's vocabulary slices (depends on V, dtype
+ *            and n_rows).
+ * The results feed ps_assemble_subtree as those of ps_score_rows do.
+ */
+size_t ps_rules_workspace_bytes(const ps_subtree_batch *batch);
+ps_status ps_score_rows_rules(const ps_subtree_batch *batch, const ps_logit_rules *rules,
+                              double *lp0, double *lq, double *entropy, int32_t *status,
+                              void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * An output head with 4-bit weights and group scales: it makes the logits rows
+ * while proposals are decoded, one row for each sequence that decodes.
+ *     logits[r][v] = sum_k hidden[r][k] * scale[v][k / group] * (q[v][k] - zero[v][k / group])
+ * q - zero is exact, products and sums are float32, scales are applied to each
+ * group's (or each 128 elements') sum; a bfloat16 result is rounded once.
+ *
+ * V, K         vocabulary and hidden size; K is a multiple of group.
+ * group        32, 64, or a multiple of 128.
+ * scale_dtype  ps_dtype of scales.
+ * q            [V][K/2] bytes: byte j of a row holds element 2j in its low four
+ *              bits and element 2j+1 in its high four; 16-byte aligned.
+ * scales       [V][K/group].
+ * zeros        [V][K/group] bytes, values 0..15 (the low four bits are read), or
+ *              NULL: every zero is 8.
+ */
+typedef struct {
+    int32_t V;
+    int32_t K;
+    int32_t group;
+    int32_t scale_dtype;
+    const uint8_t *q;
+    const void *scales;
+    const uint8_t *zeros;
+} ps_head;
+
+/*
+ * hidden  [n_rows][hidden_ld] bfloat16, 16-byte aligned rows (hidden_ld a
+ *         multiple of 8, >= K).
+ * logits  [n_rows][ld] of dtype (PS_BF16 or PS_F32), rows as in
+ *         ps_subtree_batch; elements V..ld-1 of a row are not written.
+ * n_rows == 0 does nothing.
+ */
+ps_status ps_head_rows(const ps_head *head, const void *hidden, int64_t hidden_ld, int32_t n_rows,
+                       void *logits, int64_t ld, int32_t dtype, void *cuda_stream);
 
 /* Static text for a status code. */
 const char *ps_status_string(ps_status status);

@@ -10,10 +10,11 @@ Entry points (see include/ps.h for the contract):
     ps_score_workspace_bytes, ps_score_subtree, ps_score_rows,
     ps_assemble_subtree, ps_walk_subtree, ps_score_walk_subtree, ps_carry_state,
     ps_validate_subtree,
-    ps_score_subtree_noalloc, ps_status_string, ps_version
+    ps_score_subtree_noalloc, ps_status_string, ps_version,
+    ps_process_rows, ps_rules_workspace_bytes, ps_score_rows_rules, ps_head_rows
 Convenience: ``make_batch``, ``make_score_out``, ``make_tree``,
-``make_walk_out`` build the structs from tensors; ``DeviceSubtree`` holds a
-whole batch on the GPU with its outputs and workspace.
+``make_walk_out``, ``make_rules``, ``make_head`` build the structs from tensors;
+``DeviceSubtree`` holds a whole batch on the GPU with its outputs and workspace.
 """
 
 from __future__ import annotations
@@ -36,6 +37,7 @@ PS_BF16, PS_F32 = 0, 1
 PS_DEV_BITS = {
     0x01: "BAD_TOKEN", 0x02: "NONFINITE", 0x04: "INFEASIBLE", 0x08: "BAD_TREE",
     0x10: "BAD_LAYOUT", 0x20: "TIMEOUT", 0x40: "BAD_ROW_INDEX", 0x80: "BAD_UNIFORM",
+    0x100: "BAD_RULES",
 }
 PS_NODE_LEAF, PS_NODE_DEFERRED = -1, -2
 
@@ -74,6 +76,20 @@ class PsCarryIo(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("state_seg", "row_lp0", "row_lq", "row_entropy", "prev_lp0",
                                    "prev_lq", "prev_entropy", "next_lp0", "next_lq",
                                    "next_entropy", "loglik", "confidence", "status")]
+
+
+class PsLogitRules(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_masks", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int64), ("n_bias", ctypes.c_int64),
+                ("mask_ld", ctypes.c_int64)] + \
+        [(n, _vp) for n in ("seq_begin", "seq_tokens", "seq_prompt", "repetition", "frequency",
+                            "presence", "bias_begin", "bias_ids", "bias_values", "mask",
+                            "row_seq", "row_len", "row_mask")]
+
+
+class PsHead(ctypes.Structure):
+    _fields_ = [("V", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("q", _vp), ("scales", _vp), ("zeros", _vp)]
 
 
 class PsError(RuntimeError):
@@ -138,6 +154,19 @@ def lib() -> ctypes.CDLL:
         L.ps_selftest_wait_timeout.restype = ctypes.c_int
         L.ps_selftest_read.argtypes = [_vp, ctypes.c_size_t, _vp, _vp]
         L.ps_selftest_read.restype = ctypes.c_int
+        L.ps_process_rows.argtypes = [ctypes.POINTER(PsLogitRules), ctypes.c_int32,
+                                      ctypes.c_int32, ctypes.c_int64, _vp, ctypes.c_int64, _vp,
+                                      ctypes.c_int64, _vp, _vp]
+        L.ps_process_rows.restype = ctypes.c_int
+        L.ps_rules_workspace_bytes.argtypes = [ctypes.POINTER(PsSubtreeBatch)]
+        L.ps_rules_workspace_bytes.restype = ctypes.c_size_t
+        L.ps_score_rows_rules.argtypes = [ctypes.POINTER(PsSubtreeBatch),
+                                          ctypes.POINTER(PsLogitRules), _vp, _vp, _vp, _vp, _vp,
+                                          ctypes.c_size_t, _vp]
+        L.ps_score_rows_rules.restype = ctypes.c_int
+        L.ps_head_rows.argtypes = [ctypes.POINTER(PsHead), _vp, ctypes.c_int64, ctypes.c_int32,
+                                   _vp, ctypes.c_int64, ctypes.c_int32, _vp]
+        L.ps_head_rows.restype = ctypes.c_int
         L.ps_status_string.argtypes = [ctypes.c_int]
         L.ps_status_string.restype = ctypes.c_char_p
         L.ps_version.argtypes = []
@@ -288,6 +317,65 @@ def ps_carry_state(batch: PsSubtreeBatch, io: PsCarryIo, stream=None, check: boo
     return st
 
 
+def ps_process_rows(rules: PsLogitRules, logits: torch.Tensor, out: torch.Tensor,
+                    status: torch.Tensor, V: int | None = None, stream=None,
+                    check: bool = True) -> int:
+    """out[r] = the rules applied to logits[r] (see include/ps.h); out may be
+    logits itself.  V: ids of a row (default: the row length)."""
+    dt = _row_dtype(logits, "logits")
+    _need(out, logits.dtype, "out")
+    _need(status, torch.int32, "status")
+    if logits.dim() != 2 or out.dim() != 2 or out.shape[0] != logits.shape[0]:
+        raise ValueError("logits and out must be [n_rows, ld] with the same n_rows")
+    n_rows, ld, out_ld = logits.shape[0], logits.shape[1], out.shape[1]
+    _need_rows(rules, n_rows)
+    st = lib().ps_process_rows(ctypes.byref(rules), ld if V is None else int(V), dt, n_rows,
+                               _ptr(logits), ld, _ptr(out), out_ld, _ptr(status),
+                               _stream(stream, logits))
+    if check and st != PS_OK:
+        raise PsError(st, "ps_process_rows")
+    return st
+
+
+def ps_rules_workspace_bytes(batch: PsSubtreeBatch) -> int:
+    return int(lib().ps_rules_workspace_bytes(ctypes.byref(batch)))
+
+
+def ps_score_rows_rules(batch: PsSubtreeBatch, rules: PsLogitRules, lp0: torch.Tensor,
+                        lq: torch.Tensor, status: torch.Tensor, workspace: torch.Tensor,
+                        stream=None, check: bool = True,
+                        entropy: torch.Tensor | None = None) -> int:
+    """ps_score_rows under rules, without writing the processed rows; the
+    workspace holds ps_rules_workspace_bytes(batch)."""
+    _need(lp0, torch.float64, "lp0")
+    _need(lq, torch.float64, "lq")
+    _need(entropy, torch.float64, "entropy", optional=True)
+    _need(status, torch.int32, "status")
+    _need_rows(rules, batch.n_rows)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    st = lib().ps_score_rows_rules(ctypes.byref(batch), ctypes.byref(rules), _ptr(lp0), _ptr(lq),
+                                   _ptr(entropy), _ptr(status), _ptr(workspace), ws_bytes,
+                                   _stream(stream, workspace))
+    if check and st != PS_OK:
+        raise PsError(st, "ps_score_rows_rules")
+    return st
+
+
+def ps_head_rows(head: PsHead, hidden: torch.Tensor, logits: torch.Tensor, stream=None,
+                 check: bool = True) -> int:
+    """logits[:, :V] = hidden times the 4-bit head (see include/ps.h): hidden is
+    [n_rows, >= K] bfloat16, logits [n_rows, ld] bfloat16 or float32."""
+    _need(hidden, torch.bfloat16, "hidden")
+    dt = _row_dtype(logits, "logits")
+    if hidden.dim() != 2 or logits.dim() != 2 or hidden.shape[0] != logits.shape[0]:
+        raise ValueError("hidden and logits must be matrices with the same number of rows")
+    st = lib().ps_head_rows(ctypes.byref(head), _ptr(hidden), hidden.shape[1], hidden.shape[0],
+                            _ptr(logits), logits.shape[1], dt, _stream(stream, logits))
+    if check and st != PS_OK:
+        raise PsError(st, "ps_head_rows")
+    return st
+
+
 def make_carry_io(*, state_seg, row_lp0, row_lq, next_lp0, next_lq, status, row_entropy=None,
                   prev_lp0=None, prev_lq=None, prev_entropy=None, next_entropy=None,
                   loglik=None, confidence=None) -> PsCarryIo:
@@ -404,6 +492,83 @@ def _need(x, dtype: torch.dtype, name: str, optional: bool = False):
             raise TypeError(f"{name} must be {_NP_OF[dtype]}, got {x.dtype}")
     else:
         raise TypeError(f"{name}: tensor or ndarray expected")
+
+
+def _row_dtype(x, name: str) -> int:
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be a bf16 or f32 tensor")
+    return PS_BF16 if x.dtype == torch.bfloat16 else PS_F32
+
+
+def _need_rows(rules: PsLogitRules, n_rows: int) -> None:
+    have = rules._rows
+    if have is not None and have < n_rows:
+        raise ValueError(f"the rules' row arrays hold {have} rows, {n_rows} are asked for")
+
+
+def make_rules(*, seq_begin=None, seq_tokens=None, seq_prompt=None, repetition=None,
+               frequency=None, presence=None, bias_begin=None, bias_ids=None, bias_values=None,
+               mask=None, row_seq=None, row_len=None, row_mask=None) -> PsLogitRules:
+    """Fill a ps_logit_rules from device tensors (see include/ps.h).  mask is
+    [n_masks, words] int32 holding the 32-bit words; every argument may be left
+    out where the C struct takes NULL."""
+    i32 = (("seq_tokens", seq_tokens), ("seq_prompt", seq_prompt), ("bias_ids", bias_ids),
+           ("mask", mask), ("row_seq", row_seq), ("row_len", row_len), ("row_mask", row_mask))
+    i64 = (("seq_begin", seq_begin), ("bias_begin", bias_begin))
+    f32 = (("repetition", repetition), ("frequency", frequency), ("presence", presence),
+           ("bias_values", bias_values))
+    u = PsLogitRules()
+    for group, dt in ((i32, torch.int32), (i64, torch.int64), (f32, torch.float32)):
+        for name, x in group:
+            _need(x, dt, name, optional=True)
+            setattr(u, name, _ptr(x))
+    size = lambda x: 0 if x is None else int(x.shape[0])
+    if seq_begin is None and any(x is not None for x in (seq_tokens, seq_prompt, repetition,
+                                                         frequency, presence)):
+        raise ValueError("a history and penalties need seq_begin")
+    if (seq_begin is None) != (seq_tokens is None):
+        raise ValueError("seq_begin and seq_tokens go together")
+    if len({x is None for x in (bias_begin, bias_ids, bias_values)}) != 1:
+        raise ValueError("bias_begin, bias_ids and bias_values go together")
+    if bias_ids is not None and size(bias_ids) != size(bias_values):
+        raise ValueError("bias_ids and bias_values must have the same length")
+    per_seq = [x for x in (seq_begin, bias_begin) if x is not None]
+    u.n_seqs = size(per_seq[0]) - 1 if per_seq else 0
+    if any(size(x) < 1 for x in per_seq) or any(size(x) != size(per_seq[0]) for x in per_seq) or any(
+            size(x) != u.n_seqs for x in (seq_prompt, repetition, frequency, presence)
+            if x is not None):
+        raise ValueError("the arrays of the sequences differ in length")
+    u.n_tokens, u.n_bias = size(seq_tokens), size(bias_ids)
+    if mask is not None:
+        if mask.dim() != 2:
+            raise ValueError("mask must be [n_masks, words]")
+        u.n_masks, u.mask_ld = int(mask.shape[0]), int(mask.shape[1])
+    elif row_mask is not None:
+        raise ValueError("row_mask needs mask")
+    rows = [size(x) for x in (row_seq, row_len, row_mask) if x is not None]
+    u._rows = min(rows) if rows else None
+    u._keep = (seq_begin, seq_tokens, seq_prompt, repetition, frequency, presence, bias_begin,
+               bias_ids, bias_values, mask, row_seq, row_len, row_mask)
+    return u
+
+
+def make_head(*, q: torch.Tensor, scales: torch.Tensor, group: int,
+              zeros: torch.Tensor | None = None) -> PsHead:
+    """Fill a ps_head from device tensors: q [V, K/2] uint8, scales [V, K/group]
+    bfloat16 or float32, zeros [V, K/group] uint8 or None."""
+    if q.dtype != torch.uint8 or q.dim() != 2:
+        raise TypeError("q must be a [V, K/2] uint8 tensor")
+    h = PsHead()
+    h.V, h.K, h.group = int(q.shape[0]), 2 * int(q.shape[1]), int(group)
+    h.scale_dtype = _row_dtype(scales, "scales")
+    shape = (h.V, h.K // h.group) if h.group > 0 and h.K % h.group == 0 else None
+    if tuple(scales.shape) != shape:
+        raise ValueError("scales must be [V, K / group]")
+    if zeros is not None and (zeros.dtype != torch.uint8 or tuple(zeros.shape) != shape):
+        raise ValueError("zeros must be [V, K / group] uint8")
+    h.q, h.scales, h.zeros = _ptr(q), _ptr(scales), _ptr(zeros)
+    h._keep = (q, scales, zeros)
+    return h
 
 
 def make_batch(*, V: int, T: int, alpha: float, tau: float, chain_seg0, seg_row0, seg_cut,

@@ -8,13 +8,13 @@
 #include <mutex>
 #include <vector>
 
+#include "ps_api.cuh"
 #include "ps_internal.cuh"
 
 namespace {
 
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+using ps::align_up;
+using ps::kAlign;
 
 // Workspace: per-row values (when the caller does not ask for them), the
 // split-row partials, then the per-chain arrival counters of the fused
@@ -41,6 +41,10 @@ WsLayout ws_layout(int64_t n_rows, int32_t n_chains) {
     w.total = w.cnt_off + w.cnt_bytes;
     return w;
 }
+
+}  // namespace
+
+namespace ps {
 
 int elem_size(int32_t dtype) { return dtype == PS_BF16 ? 2 : (dtype == PS_F32 ? 4 : 0); }
 
@@ -93,7 +97,7 @@ int32_t integer_power(double tau) {
     return 0;
 }
 
-ps_status check_batch_host(const ps_subtree_batch *b, bool need_data = true) {
+ps_status check_batch_host(const ps_subtree_batch *b, bool need_data) {
     if (!b) return PS_ERR_INVALID_ARG;
     if (b->V < 1 || b->T < 1 || b->n_chains < 1 || b->n_seg < b->n_chains || b->n_rows < 0)
         return PS_ERR_INVALID_ARG;
@@ -117,11 +121,13 @@ ps_status check_batch_host(const ps_subtree_batch *b, bool need_data = true) {
     return PS_OK;
 }
 
-}  // namespace
+}  // namespace ps
+
+using namespace ps;
 
 extern "C" {
 
-const char *ps_version(void) { return "libps 0.4.0 (sm_103a)"; }
+const char *ps_version(void) { return "libps 0.5.0 (sm_103a)"; }
 
 const char *ps_status_string(ps_status s) {
     switch (s) {
