@@ -35,6 +35,22 @@ ps_status check_rules_host(const ps_logit_rules *u, int32_t V, int64_t n_rows) {
     return PS_OK;
 }
 
+// Workspace of ps_score_rows_rules.
+struct ScoreWs {
+    RuleCut cut;
+    size_t tok_off, bad_off, total;
+};
+
+ScoreWs score_ws(const ps_subtree_batch *b) {
+    ScoreWs w;
+    w.cut = score_cut(b->V, b->dtype, b->n_rows);
+    const size_t n = (size_t)b->n_rows;
+    w.tok_off = align_up(n * w.cut.n_slices * kScoreParts * sizeof(ChunkPart), kAlign);
+    w.bad_off = w.tok_off + align_up(n * sizeof(float), kAlign);
+    w.total = w.bad_off + align_up(n * sizeof(int32_t), kAlign);
+    return w;
+}
+
 int32_t slices_of(int32_t V, int32_t dtype) {
     const int32_t s = rules_slice_ids(dtype);
     return (int32_t)(((int64_t)V + s - 1) / s);
@@ -81,7 +97,7 @@ ps_status ps_process_rows(const ps_logit_rules *rules, int32_t V, int32_t dtype,
 
 size_t ps_rules_workspace_bytes(const ps_subtree_batch *b) {
     if (!b || b->n_rows <= 0 || b->V < 1 || elem_size(b->dtype) == 0) return kAlign;
-    return align_up((size_t)b->n_rows * slices_of(b->V, b->dtype) * sizeof(SlicePart), kAlign);
+    return score_ws(b).total;
 }
 
 ps_status ps_score_rows_rules(const ps_subtree_batch *b, const ps_logit_rules *rules, double *lp0,
@@ -103,8 +119,11 @@ ps_status ps_score_rows_rules(const ps_subtree_batch *b, const ps_logit_rules *r
     p.r.n_rows = b->n_rows;
     p.r.V = b->V;
     p.r.status = status;
-    p.n_slices = slices_of(b->V, b->dtype);
-    p.parts = (SlicePart *)workspace;
+    const ScoreWs ws = score_ws(b);
+    p.cut = ws.cut;
+    p.parts = (ChunkPart *)workspace;
+    p.tok_logit = (float *)((uint8_t *)workspace + ws.tok_off);
+    p.row_bad = (int32_t *)((uint8_t *)workspace + ws.bad_off);
     RowsParams &q = p.rows;
     const int esz = elem_size(b->dtype);
     q.logits = (const uint8_t *)b->logits;
@@ -116,6 +135,7 @@ ps_status ps_score_rows_rules(const ps_subtree_batch *b, const ps_logit_rules *r
     q.V = b->V;
     q.dtype = b->dtype;
     q.flags = b->flags;
+    q.row_bytes = (int32_t)(((int64_t)b->V * esz + 15) / 16 * 16);
     q.npow = integer_power(b->tau);
     q.g = (float)(1.0 / b->tau);
     q.lp0 = lp0;

@@ -22,19 +22,28 @@ struct ProcessParams {
     int32_t n_slices;
 };
 
-// Sums of one vocabulary slice of a row (ps_row_sums.cuh has their meaning).
-struct __align__(16) SlicePart {
+// How the vocabulary is cut for the kernels that stream rows.
+struct RuleCut {
+    int32_t ids;                // of a slice, a multiple of 128
+    int32_t n_slices;
+};
+// most: ids of a slice at most (a multiple of 128).
+RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows);
+RuleCut score_cut(int32_t V, int32_t dtype, int64_t n_rows);
+constexpr int kScoreParts = 16;     // partial sums of a slice of a row
+
+// Sums of one warp's ids of a slice (ps_row_sums.cuh has their meaning).
+struct __align__(16) ChunkPart {
     float R, s1, st, y1;
-    float ltok;
-    int32_t bad;                // the row failed a check; its bits are set
-    int32_t pad[2];
 };
 
 struct ScoreRulesParams {
     RulesParams r;
     RowsParams rows;            // logits, tokens, row_index, outputs, tau
-    int32_t n_slices;
-    SlicePart *parts;           // [n_rows][n_slices]
+    RuleCut cut;
+    ChunkPart *parts;           // [n_rows][n_slices][kScoreParts]
+    float *tok_logit;           // [n_rows] the token's processed logit
+    int32_t *row_bad;           // [n_rows] status bits
 };
 
 cudaError_t launch_process_rows(const ProcessParams &p, int32_t dtype, int sms,
@@ -57,6 +66,7 @@ struct RowRules {
     const float *bias_values;
     const uint32_t *mask;       // its mask row, or nullptr
     int32_t len;                // tokens of history
+    int32_t len_all;            // tokens of its sequence
     int32_t prompt;             // the first of them that were not generated
     int32_t n_bias;
     float rho, freq, pres;
@@ -65,7 +75,7 @@ struct RowRules {
 
 __device__ __forceinline__ bool finite_f(float x) { return fabsf(x) < INFINITY; }
 
-__device__ RowRules row_rules(const RulesParams &p, int64_t r) {
+__device__ __forceinline__ RowRules row_rules(const RulesParams &p, int64_t r) {
     const ps_logit_rules &u = p.rules;
     RowRules o{};
     o.rho = 1.f;
@@ -78,11 +88,12 @@ __device__ RowRules row_rules(const RulesParams &p, int64_t r) {
             if (u.seq_begin) {
                 const int64_t b = __ldg(u.seq_begin + s), e = __ldg(u.seq_begin + s + 1);
                 const int64_t n = u.row_len ? (int64_t)__ldg(u.row_len + r) : e - b;
-                if (b < 0 || e < b || e > u.n_tokens || n < 0 || n > e - b || n > 0x7fffffff) {
+                if (b < 0 || e < b || e > u.n_tokens || n < 0 || n > e - b || e - b > 0x7fffffff) {
                     o.bad |= PS_DEV_BAD_RULES;
                 } else {
                     o.hist = u.seq_tokens + b;
                     o.len = (int32_t)n;
+                    o.len_all = (int32_t)(e - b);
                     o.prompt = u.seq_prompt ? __ldg(u.seq_prompt + s) : 0;
                 }
                 if (u.repetition) o.rho = __ldg(u.repetition + s);

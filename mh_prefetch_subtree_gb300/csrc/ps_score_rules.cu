@@ -1,43 +1,136 @@
 // log p0, log q_tau and entropy of each row's token under rules
 // (ps_score_rows_rules), without writing the processed rows.
 //
-// A block takes one slice of one row: it masks the slice on its way into shared
-// memory, takes the token and the ids that penalties or biases touch out of it
-// (their places become -inf, their processed float32 values are added on their
-// own, so nothing is rounded to the rows' type), and sums the rest.  A second
-// kernel joins the slices' sums of each row.
-#include "ps_row_sums.cuh"
-#include "ps_rules.cuh"
+// The formulation is ps_score_rows.cu's: sums relative to a reference, the token
+// left out.  ps_rule_rows.cuh brings the rows to the consumer warps.  In the
+// stage a warp takes the token and the ids that penalties or biases touch out
+// (their places become -inf) and adds their processed float32 values on their
+// own, so nothing is rounded to the rows' type.  It then reads its ids into
+// registers, gives the stage back, applies the mask and sums.  What is left are 16
+// partial sums for each slice of a row, which a second kernel joins in their
+// order.
+//
+// Where a mask leaves a lane at most kFewIds of its 64 (32 for float32) ids, the
+// warp steps through the allowed ones instead of exponentiating all; where it
+// leaves few of the slice, only their vectors are read from memory.
+//
+// The reference only has to keep the exponentials in range, so without entropy
+// the warp keeps the one of the row before and looks for its ids' maximum only when
+// the sums leave [2^-60, 2^64].  With entropy the sum of 2^y y cancels the more the
+// further the reference is from the maximum, so each row takes its own.
+#include "ps_rule_rows.cuh"
 
 namespace ps {
 namespace {
 
-// Adds one processed logit to the running sums.
+constexpr int kRing = 2;
+constexpr int kFewIds = 10;
+constexpr float kLeast = 8.673617379884035e-19f;     // 2^-60
+
+template <int DT>
+struct ScoreSmem : RuleSmem<DT, DT == PS_BF16 ? 2 : 1, kRing> {
+    uint4 lut[DT == PS_BF16 ? 256 : 16];             // mask bits -> which words stay
+};
+
+__device__ __forceinline__ float warp_max_nan(float m) {
+    float d;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(m));
+    return d;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// 2^(g y) from y and e = 2^y.
+template <int NP>
+__device__ __forceinline__ float tau_term(float y, float e, float g) {
+    if constexpr (NP == 0) return ex2(g * y);
+    else if constexpr (NP == 1) return e;
+    else if constexpr (NP == 2) return e * e;
+    else if constexpr (NP == 4) return (e * e) * (e * e);
+    else return ((e * e) * (e * e)) * ((e * e) * (e * e));
+}
+
+// Sums relative to a reference, by lane.
+struct Sums {
+    float s1, st, y1;
+};
+
 template <int NP, bool ENT>
-__device__ __forceinline__ void add_value(Acc &a, float l, float g) {
-    if (l == -INFINITY) return;
-    const float x = l * kLog2e;
-    if (!(x <= a.R)) a = rebase<NP, ENT>(a, x, g);     // a NaN goes in here and stays
-    const float y = x - a.R, e = ex2(y);
+__device__ __forceinline__ void add_term(Sums &a, float y, float g) {
+    const float e = ex2(y);
     a.s1 += e;
-    if constexpr (NP == 0) a.st[0] += ex2(g * y);
-    else if constexpr (NP != 1) a.st[0] += ex2((float)NP * y);
+    if constexpr (NP != 1) a.st += tau_term<NP>(y, e, g);
     if constexpr (ENT) a.y1 = fmaf(e, y, a.y1);
 }
 
-template <int DT, int VPT>
-__device__ __forceinline__ float max_of(const uint4 (&q)[VPT]) {
+template <int DT>
+__device__ __forceinline__ void pairs_of(uint4 q, float2 (&v)[DT == PS_BF16 ? 4 : 2]) {
+    if constexpr (DT == PS_BF16) {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+    } else {
+        v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+        v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+    }
+}
+
+// The sums of eight vectors.
+template <int DT, int NP, bool ENT>
+__device__ __forceinline__ Sums sum_dense(const uint4 (&q)[8], float ref, float g) {
+    constexpr int kPairs = DT == PS_BF16 ? 4 : 2;
+    const float2 L2 = make_float2(kLog2e, kLog2e), nR2 = make_float2(-ref, -ref);
+    const float2 GL2 = make_float2(g * kLog2e, g * kLog2e), nGR2 = make_float2(-g * ref, -g * ref);
+    float2 a1[4], at[4], ay[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a1[j] = at[j] = ay[j] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float2 v[kPairs];
+        pairs_of<DT>(q[i], v);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const int c = kPairs == 4 ? j : (i & 1) * 2 + j;
+            const float2 x = __ffma2_rn(v[j], L2, nR2);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            a1[c] = __fadd2_rn(a1[c], e);
+            if constexpr (ENT) ay[c] = __ffma2_rn(e, x, ay[c]);
+            if constexpr (NP == 0) {
+                const float2 z = __ffma2_rn(v[j], GL2, nGR2);
+                at[c] = __fadd2_rn(at[c], make_float2(ex2(z.x), ex2(z.y)));
+            } else if constexpr (NP != 1) {
+                float2 f = e;
+                if constexpr (NP >= 4) f = __fmul2_rn(f, f);
+                if constexpr (NP >= 8) f = __fmul2_rn(f, f);
+                at[c] = __ffma2_rn(f, f, at[c]);
+            }
+        }
+    }
+    Sums s;
+    s.s1 = hsum4(a1);
+    s.st = NP == 1 ? s.s1 : hsum4(at);
+    s.y1 = ENT ? hsum4(ay) : 0.f;
+    return s;
+}
+
+template <int DT>
+__device__ __forceinline__ float max_of(const uint4 (&q)[8]) {
     if constexpr (DT == PS_BF16) {
         uint32_t m = 0xff80ff80u;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+        for (int i = 0; i < 8; ++i)
             m = max_nan_bf16x2(max_nan_bf16x2(max_nan_bf16x2(m, q[i].x), max_nan_bf16x2(q[i].y, q[i].z)),
                                q[i].w);
         return max_nan_f32(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     } else {
         float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+        for (int i = 0; i < 8; ++i)
             m = max_nan_f32(max_nan_f32(max_nan_f32(m, __uint_as_float(q[i].x)),
                                         max_nan_f32(__uint_as_float(q[i].y), __uint_as_float(q[i].z))),
                             __uint_as_float(q[i].w));
@@ -45,145 +138,302 @@ __device__ __forceinline__ float max_of(const uint4 (&q)[VPT]) {
     }
 }
 
-template <int DT, int NP, bool ENT>
-__global__ void __launch_bounds__(kRuleThreads) score_rules_kernel(const ScoreRulesParams p) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int kEsz = DT == PS_BF16 ? 2 : 4;
-    constexpr int kVec = 16 / kEsz;
-    constexpr int kVpt = kSliceIds / kVec / kRuleThreads;
-    uint4 *stage = reinterpret_cast<uint4 *>(smem);
-    uint8_t *stage_b = smem;
-    SliceTable &t = *reinterpret_cast<SliceTable *>(smem + kSliceIds * kEsz);
-    __shared__ Acc warp_acc[kRuleThreads / 32];
-    __shared__ float tok_logit;
-    const int tid = threadIdx.x;
-    const int32_t V = p.r.V;
-    const float g = p.rows.g;
-    const int64_t n_tasks = p.r.n_rows * p.n_slices;
-    for (int64_t task = blockIdx.x; task < n_tasks; task += gridDim.x) {
-        const int64_t r = task / p.n_slices;
-        const int32_t v0 = (int32_t)(task - r * p.n_slices) * kSliceIds;
-        const int32_t n = min(kSliceIds, V - v0);
-        const int32_t tok = __ldg(p.rows.tokens + r);
-        int64_t src_row = p.rows.row_index ? __ldg(p.rows.row_index + r) : r;
-        RowRules w = row_rules(p.r, r);
-        if (tok < 0 || tok >= V) w.bad |= PS_DEV_BAD_TOKEN;
-        if (src_row < 0 || src_row >= p.rows.n_logit_rows) w.bad |= PS_DEV_BAD_ROW_INDEX;
-        if (tid == 0) tok_logit = __uint_as_float(kAbsent);
-        w.bad |= build_table(t, w, V, v0);
-        SlicePart part{};
-        if (w.bad) {
-            if (tid == 0) {
-                if (v0 == 0) set_status(p.r.status, w.bad);
-                part.bad = 1;
-                p.parts[task] = part;
-            }
-            __syncthreads();
-            continue;
-        }
-        const uint8_t *src = p.rows.logits + src_row * p.rows.ld_bytes;
-        for (int i = tid; i < kSliceIds / kVec; i += blockDim.x) {
-            const int32_t v = v0 + i * kVec;
-            uint4 q = make_uint4(0, 0, 0, 0);
-            uint32_t m = 0;
-            if (i * kVec < n) {
-                m = mask_bits<kVec>(w.mask, v, V);
-                q = *reinterpret_cast<const uint4 *>(src + (int64_t)v * kEsz);
-            }
-            stage[i] = masked_vec<DT>(q, m);
-        }
-        __syncthreads();
-        Acc acc = acc_empty();
-        auto take = [&](uint32_t o, uint32_t count, float bias) {
-            const float l = penalised(load_elem<DT>(stage_b, o), count, w) + bias;
-            store_elem<DT>(stage_b, o, -INFINITY);
-            if (v0 + (int32_t)o == tok) tok_logit = l;
-            else add_value<NP, ENT>(acc, l, g);
-        };
-        for_seen(t, [&](uint32_t o) {
-            if (!is_biased(t, o)) take(o, t.count[o], 0.f);
-        });
-        for (int i = tid; i < w.n_bias; i += blockDim.x) {
-            const uint32_t o = (uint32_t)(__ldg(w.bias_ids + i) - v0);
-            if (o >= (uint32_t)kSliceIds) continue;
-            // a masked id stays -inf whatever its bias
-            if (mask_allows(w.mask, v0 + (int32_t)o)) take(o, t.count[o], __ldg(w.bias_values + i));
-            else take(o, 0, 0.f);
-        }
-        const uint32_t to = (uint32_t)(tok - v0);
-        if (tid == 0 && to < (uint32_t)kSliceIds && t.count[to] == 0 && !is_biased(t, to)) take(to, 0, 0.f);
-        __syncthreads();
-        uint4 q[kVpt];
+// Raises -inf to the floor, which keeps 2^y y finite.
+template <int DT>
+__device__ __forceinline__ void raise_floor(uint4 (&q)[8]) {
 #pragma unroll
-        for (int i = 0; i < kVpt; ++i) q[i] = stage[tid + i * kRuleThreads];
-        const float m = max_of<DT, kVpt>(q);
-        if (m != -INFINITY) {
-            Acc b = acc_empty();
-            b.R = m * kLog2e;
-            float cy;
-            sum_vecs<DT, NP, ENT, kVpt>(q, b.R, g, b.s1, b.st, cy);
-            b.y1 = cy;
-            acc = merge_part<NP, ENT>(acc, b, g);
+    for (int i = 0; i < 8; ++i) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(&q[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == PS_BF16) w[j] = max_nan_bf16x2(w[j], kFloorBf16x2);
+            else w[j] = __float_as_uint(max_nan_f32(__uint_as_float(w[j]), kFloorF32));
         }
-        acc = warp_merge<NP, ENT>(acc, g);
-        if ((tid & 31) == 0) warp_acc[tid >> 5] = acc;
-        __syncthreads();
-        if (tid < 32) {
-            acc = tid < kRuleThreads / 32 ? warp_acc[tid] : acc_empty();
-            acc = warp_merge<NP, ENT>(acc, g);
-            if (tid == 0) {
-                part.R = acc.R;
-                part.s1 = acc.s1;
-                part.st = acc.st[0];
-                part.y1 = acc.y1;
-                part.ltok = tok_logit;
-                p.parts[task] = part;
-            }
-        }
-        __syncthreads();
     }
 }
 
-// One warp a row: its slices' sums joined in slice order, then the results.
-template <int NP, bool ENT>
-__global__ void __launch_bounds__(kRuleThreads) score_rules_join_kernel(const ScoreRulesParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * (kRuleThreads / 32) + (threadIdx.x >> 5);
-    if (r >= p.r.n_rows) return;
-    Acc a = acc_empty();
-    float lt = __uint_as_float(kAbsent);
-    bool bad = false;
-    for (int i = lane; i < p.n_slices; i += 32) {
-        const SlicePart s = p.parts[r * p.n_slices + i];
-        bad |= s.bad != 0;
-        if (bad) continue;
-        a = merge_part<NP, ENT>(a, Acc{s.R, s.s1, {s.st, 0.f, 0.f}, s.y1}, p.rows.g);
-        if (__float_as_uint(s.ltok) != kAbsent) lt = s.ltok;
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    a = warp_merge<NP, ENT>(a, p.rows.g);
+template <int DT, int NP, bool ENT>
+__global__ void __launch_bounds__(kRuleWarps * 32 + 32, 1) score_rules_kernel(
+    const __grid_constant__ ScoreRulesParams p) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    using Smem = ScoreSmem<DT>;
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+    constexpr int kNb = DT == PS_BF16 ? 2 : 1;
+    constexpr int kEsz = Smem::kEsz;
+    constexpr int kVec = 16 / kEsz;                  // ids of a 16-byte vector
+    constexpr int kBv = kBlockIds / kVec;            // vectors of a block: 4 or 8
+    // the places of ids that do not count: -inf, or with entropy a large negative
+    // value, which keeps 2^y y finite
+    constexpr uint32_t kOff = ENT ? Elem<DT>::kFloorWord : Elem<DT>::kNegInfWord;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const float g = p.rows.g;
+
+    for (int i = threadIdx.x; i < (DT == PS_BF16 ? 256 : 16); i += blockDim.x) {
+        uint32_t k[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float other = __shfl_xor_sync(0xffffffffu, lt, o);
-        if (__float_as_uint(lt) == kAbsent) lt = other;
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == PS_BF16)
+                k[j] = ((i >> (2 * j)) & 1 ? 0xffffu : 0u) | ((i >> (2 * j + 1)) & 1 ? 0xffff0000u : 0u);
+            else
+                k[j] = (i >> j) & 1 ? 0xffffffffu : 0u;
+        }
+        sm.lut[i] = make_uint4(k[0], k[1], k[2], k[3]);
     }
-    if (lane == 0) finalize_row<NP, ENT>(p.rows, r, a, lt, bad);
+    rule_smem_init<Smem, kRing>(sm, 1);
+    __syncthreads();
+
+    if (wid == kRuleWarps) {
+        rule_producer<DT, kNb, kRing, true>(sm, p.r, p.cut, p.rows.logits, p.rows.ld_bytes,
+                                            p.rows.row_bytes, p.rows.row_index, p.rows.n_logit_rows,
+                                            p.rows.tokens, sm.empty);
+        return;
+    }
+
+    const RuleSpan span(p.r.n_rows, p.cut.n_slices);
+    RuleWalk<Smem> walk(sm, p.r);
+    int64_t r = span.t0 % span.rows;
+    int32_t slice = (int32_t)(span.t0 / span.rows);
+    walk.enter_slice(slice, p.cut);
+    float ref = 0.f;                                  // the warp's reference
+    int s = 0;
+    uint32_t lap = 0;
+    for (int64_t t = span.t0; t < span.t1; ++t) {
+        if (!mbar_wait_bounded(&sm.full[s], lap & 1u, kRuleWaitNs)) {
+            if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
+            return;
+        }
+        uint8_t *buf = sm.stage[s];
+        const RowDesc &desc = sm.desc[s];
+        const int4 dh = *reinterpret_cast<const int4 *>(&desc);       // tok, bad, flags, n_new
+        if ((dh.z & kDescRebuild) || dh.w) {
+            if (!walk.enter_row(s, desc)) {
+                if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
+                return;
+            }
+        }
+        const int32_t bad = dh.y | walk.bad;
+        const int32_t tok = dh.x;
+        const bool masked = dh.z & kDescMask;
+        const uint32_t *mw = sm.mask[s];
+        if (walk.s0 == 0 && wid == 0 && lane == 0) {
+            if (bad) set_status(p.r.status, bad);
+            p.row_bad[r] = bad;
+        }
+        float px = -INFINITY;                         // a touched id of this lane, and
+        Acc more = acc_empty();                       // its others
+        auto put_off = [&](uint32_t d) {
+            if constexpr (DT == PS_BF16) reinterpret_cast<uint16_t *>(buf)[d] = (uint16_t)kOff;
+            else reinterpret_cast<uint32_t *>(buf)[d] = kOff;
+        };
+        if (!bad) {
+            walk.for_touched([&](uint32_t d, float pos, float neg, float add) {
+                float l = load_elem<DT>(buf, d);
+                put_off(d);
+                l = fmaf(l, l > 0.f ? pos : neg, add);
+                if (masked && !((mw[d >> 5] >> (d & 31)) & 1u)) l = -INFINITY;
+                if ((int32_t)d == tok) {
+                    p.tok_logit[r] = l;
+                } else if (px == -INFINITY) {
+                    px = l;
+                } else if (l != -INFINITY) {
+                    const float x = l * kLog2e;
+                    if (!(x <= more.R)) more = rebase<NP, ENT>(more, x, g);       // keeps a NaN
+                    const float y = x - more.R, e = ex2(y);
+                    more.s1 += e;
+                    more.st[0] += tau_term<NP>(y, e, g);
+                    more.y1 = fmaf(e, y, more.y1);
+                }
+            });
+            if ((uint32_t)tok < (uint32_t)walk.nid && owner_of(tok) == (uint32_t)wid &&
+                !walk.is_seen(tok) && !walk.is_biased(tok) && lane == 0) {
+                p.tok_logit[r] = masked && !((mw[tok >> 5] >> (tok & 31)) & 1u)
+                                     ? -INFINITY : load_elem<DT>(buf, tok);
+                put_off(tok);
+            }
+        }
+        // ids past the vocabulary in the last block
+        if (walk.nid & 31) {
+            const uint32_t d = (uint32_t)(walk.nid & ~31) + lane;
+            if (lane >= (walk.nid & 31) && owner_of(d) == (uint32_t)wid) put_off(d);
+        }
+        __syncwarp();
+
+        uint32_t m[kNb];
+        int few = 0;
+#pragma unroll
+        for (int h = 0; h < kNb; ++h) {
+            const uint32_t b = block_of(wid, lane, h);
+            m[h] = b * kBlockIds < (uint32_t)walk.nid ? (masked ? mw[b] : 0xffffffffu) : 0u;
+            few += __popc(m[h]);
+        }
+        if (masked) few = __reduce_max_sync(0xffffffffu, few);
+        Sums sum{0.f, 0.f, 0.f};
+        const bool touched = __any_sync(0xffffffffu, px != -INFINITY);
+        // the touched ids' part relative to ref
+        auto add_touched = [&](Sums &a) {
+            if (px != -INFINITY) add_term<NP, ENT>(a, px * kLog2e - ref, g);
+            if (more.R != -INFINITY) {
+                const float d = more.R - ref, f = ex2(d);
+                a.s1 = fmaf(more.s1, f, a.s1);
+                if constexpr (NP != 1) a.st = fmaf(more.st[0], tau_term<NP>(d, f, g), a.st);
+                if constexpr (ENT) a.y1 += f * fmaf(d, more.s1, more.y1);
+            }
+        };
+        auto touched_max = [&](float x) {
+            x = max_nan_f32(x, px);
+            if (more.R == more.R) x = max_nan_f32(x, more.R * kLn2f);
+            return x;
+        };
+        auto join_lanes = [&](Sums a) {
+            sum.s1 = warp_sum(a.s1);
+            sum.st = NP == 1 ? sum.s1 : warp_sum(a.st);
+            if constexpr (ENT) sum.y1 = warp_sum(a.y1);
+        };
+        auto in_range = [&]() {
+            return sum.s1 >= kLeast && sum.s1 <= kLimit && sum.st >= kLeast && sum.st <= kLimit;
+        };
+        if (masked && few <= kFewIds) {
+            if (few > 0 || touched) {
+                // step through the allowed ids of the lane
+                auto each = [&](auto f) {
+#pragma unroll
+                    for (int h = 0; h < kNb; ++h) {
+                        const uint32_t d0 = block_of(wid, lane, h) * kBlockIds;
+                        for (uint32_t x = m[h]; x != 0; x &= x - 1)
+                            f(load_elem<DT>(buf, d0 + __ffs(x) - 1));
+                    }
+                };
+                for (bool look = ENT;;) {
+                    if (look) {
+                        float x = -INFINITY;
+                        each([&](float l) { x = max_nan_f32(x, l); });
+                        if (x <= kAbsentBelow) x = -INFINITY;
+                        x = warp_max_nan(touched_max(x));
+                        if (x == -INFINITY) {
+                            sum = Sums{0.f, 0.f, 0.f};
+                            break;
+                        }
+                        ref = x * kLog2e;
+                    }
+                    Sums a{0.f, 0.f, 0.f};
+                    each([&](float l) {
+                        const float y = fmaf(l, kLog2e, -ref);
+                        if (!(l <= kAbsentBelow)) add_term<NP, ENT>(a, y, g);
+                    });
+                    if constexpr (NP == 1) a.st = a.s1;
+                    add_touched(a);
+                    join_lanes(a);
+                    if (look || in_range()) break;
+                    look = true;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[s]);
+        } else {
+            uint4 q[8];
+#pragma unroll
+            for (int h = 0; h < kNb; ++h) {
+                const uint4 *v = reinterpret_cast<const uint4 *>(buf) + block_of(wid, lane, h) * kBv;
+#pragma unroll
+                for (int i = 0; i < kBv; ++i) {
+                    // the lanes' vectors in an order that spreads them over the banks
+                    const int at = kBv == 4 ? ((i + (lane >> 1)) & 3) : ((i + lane) & 7);
+                    q[h * kBv + i] = m[h] ? v[at] : make_uint4(kOff, kOff, kOff, kOff);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[s]);     // the stage is free
+            if (masked) {
+#pragma unroll
+                for (int h = 0; h < kNb; ++h) {
+                    // bits of vector i of the lane's order at the bottom of x
+                    uint32_t x = kBv == 4 ? __funnelshift_r(m[h], m[h], 8 * ((lane >> 1) & 3))
+                                          : __funnelshift_r(m[h], m[h], 4 * (lane & 7));
+#pragma unroll
+                    for (int i = 0; i < kBv; ++i) {
+                        const uint4 k = sm.lut[kBv == 4 ? (x >> (8 * i)) & 0xffu : (x >> (4 * i)) & 15u];
+                        uint4 &v = q[h * kBv + i];
+                        v.x = (v.x & k.x) | (kOff & ~k.x);
+                        v.y = (v.y & k.y) | (kOff & ~k.y);
+                        v.z = (v.z & k.z) | (kOff & ~k.z);
+                        v.w = (v.w & k.w) | (kOff & ~k.w);
+                    }
+                }
+            }
+            for (bool look = ENT;;) {
+                if (look) {
+                    float x = max_of<DT>(q);
+                    if (x <= kAbsentBelow) x = -INFINITY;
+                    x = warp_max_nan(touched_max(x));
+                    if (x == -INFINITY) {             // nothing here
+                        sum = Sums{0.f, 0.f, 0.f};
+                        break;
+                    }
+                    ref = x * kLog2e;
+                }
+                Sums a = sum_dense<DT, NP, ENT>(q, ref, g);
+                add_touched(a);
+                if constexpr (NP == 1) a.st = a.s1;
+                join_lanes(a);
+                if constexpr (ENT) {
+                    // a -inf among the logits makes 2^y y NaN: raise it and sum again
+                    if (!(sum.y1 == sum.y1) && sum.s1 == sum.s1) {
+                        raise_floor<DT>(q);
+                        a = sum_dense<DT, NP, ENT>(q, ref, g);
+                        add_touched(a);
+                        if constexpr (NP == 1) a.st = a.s1;
+                        join_lanes(a);
+                    }
+                }
+                if (look || in_range()) break;
+                look = true;
+            }
+        }
+        if (lane == 0)
+            p.parts[(r * p.cut.n_slices + slice) * kScoreParts + wid] =
+                ChunkPart{sum.s1 == 0.f ? -INFINITY : ref, sum.s1, sum.st, sum.y1};
+        if (++s == kRing) {
+            s = 0;
+            ++lap;
+        }
+        if (++r == span.rows) {
+            r = 0;
+            walk.enter_slice(++slice, p.cut);
+        }
+    }
+}
+
+// One warp a row: its partial sums joined in their order, then the results.
+template <int NP, bool ENT>
+__global__ void __launch_bounds__(256) score_rules_join_kernel(
+    const __grid_constant__ ScoreRulesParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (r >= p.r.n_rows) return;
+    const bool bad = p.row_bad[r] != 0;
+    const int n = p.cut.n_slices * kScoreParts;
+    Acc a = acc_empty();
+    if (!bad)
+        for (int i = lane; i < n; i += 32) {
+            const float4 s = __ldg(reinterpret_cast<const float4 *>(p.parts + r * n + i));
+            a = merge_part<NP, ENT>(a, Acc{s.x, s.y, {s.z, 0.f, 0.f}, s.w}, p.rows.g);
+        }
+    a = warp_merge<NP, ENT>(a, p.rows.g);
+    if (lane == 0) finalize_row<NP, ENT>(p.rows, r, a, bad ? 0.f : p.tok_logit[r], bad);
 }
 
 template <int DT, int NP, bool ENT>
 cudaError_t launch(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
-    const int smem = (int)sizeof(SliceTable) + kSliceIds * (DT == PS_BF16 ? 2 : 4);
+    const int smem = (int)sizeof(ScoreSmem<DT>);
     cudaError_t e = cudaFuncSetAttribute(score_rules_kernel<DT, NP, ENT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t tasks = p.r.n_rows * p.n_slices, most = (int64_t)sms * 3;
+    const int64_t tasks = p.r.n_rows * p.cut.n_slices;
     score_rules_kernel<DT, NP, ENT>
-        <<<(int)(tasks < most ? tasks : most), kRuleThreads, smem, stream>>>(p);
+        <<<(int)(tasks < sms ? tasks : sms), kRuleWarps * 32 + 32, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int64_t per = kRuleThreads / 32;
-    score_rules_join_kernel<NP, ENT>
-        <<<(int)((p.r.n_rows + per - 1) / per), kRuleThreads, 0, stream>>>(p);
+    score_rules_join_kernel<NP, ENT><<<(unsigned)((p.r.n_rows + 7) / 8), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -199,6 +449,24 @@ cudaError_t launch_np(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// As few slices as hold the vocabulary, or where there are few rows as many as
+// give every SM a block (of 1024 ids at least); all of the same size but the last.
+RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows) {
+    constexpr int64_t kBlocks = 152;
+    const int64_t least = ((int64_t)V + most - 1) / most;
+    const int64_t more = kBlocks / (n_rows > 0 ? n_rows : 1), fine = V / 1024;
+    int64_t slices = more < fine ? more : fine;
+    if (slices < least) slices = least;
+    RuleCut c;
+    c.ids = (int32_t)(((V + slices - 1) / slices + 127) / 128 * 128);
+    c.n_slices = (int32_t)(((int64_t)V + c.ids - 1) / c.ids);
+    return c;
+}
+
+RuleCut score_cut(int32_t V, int32_t dtype, int64_t n_rows) {
+    return rule_cut(V, dtype == PS_BF16 ? ScoreSmem<PS_BF16>::kIds : ScoreSmem<PS_F32>::kIds, n_rows);
+}
 
 cudaError_t launch_score_rules(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
     if (p.rows.dtype == PS_BF16)
