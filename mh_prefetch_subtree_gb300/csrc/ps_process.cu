@@ -10,7 +10,7 @@ namespace ps {
 namespace {
 
 template <int DT>
-__global__ void __launch_bounds__(kRuleThreads) process_rows_kernel(const ProcessParams p) {
+__global__ void __launch_bounds__(kTableThreads) process_rows_kernel(const ProcessParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     SliceTable &t = *reinterpret_cast<SliceTable *>(smem);
     constexpr int kEsz = DT == PS_BF16 ? 2 : 4;
@@ -69,7 +69,7 @@ cudaError_t launch(const ProcessParams &p, int sms, cudaStream_t stream) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t tasks = p.r.n_rows * p.n_slices, most = (int64_t)sms * 4;
-    process_rows_kernel<DT><<<(int)(tasks < most ? tasks : most), kRuleThreads, smem, stream>>>(p);
+    process_rows_kernel<DT><<<(int)(tasks < most ? tasks : most), kTableThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -3,22 +3,26 @@
 //
 // A block owns a slice of the vocabulary and walks down the rows, so that
 // consecutive positions of a sequence, which differ by one token of history,
-// reuse what is known about the row before.  One producer warp reads the rows'
-// entries ahead, says in a descriptor what changes from row to row, and fills a
-// ring of stages: the slice of the row's logits (bulk copies) and of its mask.
-// 16 consumer warps work on the stage.
+// reuse what is known about the row before.  A slice is every n-th segment of 2048
+// ids, since the ids that a history touches lie close together (common tokens have
+// low ids): with slices of neighbouring ids the blocks of the first slice took
+// 1.8 times as long as the others.  The block's warps have three jobs.  The
+// producers, one a stage, take the rows in turn (one alone spent 3200 cycles on a
+// row, and a row of 48 KB has about 1900), say in a descriptor what changed since the row before,
+// and fill a ring of stages: the slice of the row's logits (bulk copies) and of its
+// mask.  The patchers know which ids penalties and biases touch
+// and treat those in the stage.  The others work on all that is left, without a
+// thought for the rules but the mask.  (With the touched ids spread over the
+// warps that also sum, the sums took 620 instructions for 64 ids a lane, against
+// about 340 alone: 8000 rows of 151936 bf16 took 593 us.)
 //
-// Which warp takes which ids.  The slice is cut into blocks of 32 ids (one mask
-// word), dealt to the warps in turn: ids of common tokens lie close together, so
-// a warp that owned a long run of ids could hold most of a history (measured: 4.9
-// ms instead of 1.1 for 8000 rows of 151936 with such histories).  Lane l of warp
-// w owns blocks h 512 + 16 l + (w + l) % 16 (h = 0, 1, ...); the skew puts the
-// lanes' vectors in different banks.
-//
-// What a warp knows of its ids is in shared memory: how often each was generated
-// (16 bits), bit sets of the seen and the biased ones, and a list of both while it
-// is short.  A new token costs a few instructions in the one warp that owns it.
-// Where the sequence changes, the consumers read the whole history together.
+// What the patchers know is in shared memory: how often each id of the slice was
+// generated (16 bits), bit sets of the seen and the biased ones, and a list of both
+// while it is short.  Blocks of 32 ids (one mask word) are dealt to them in turn:
+// ids of common tokens lie close together, so a warp that owned a long run of ids
+// could hold most of a history.  A new token costs a few instructions in the one
+// warp that owns it.  Where the sequence changes, the patchers read the whole
+// history together.
 #pragma once
 
 #include "ps_row_sums.cuh"
@@ -27,64 +31,111 @@
 namespace ps {
 namespace {
 
-constexpr int kRuleWarps = 16;                       // consumers
-constexpr int kListCap = 128;                        // touched ids of a warp kept as a list
+constexpr int kSumWarps = 12;                        // work on all ids
+constexpr int kPatchWarps = 4;
+constexpr int kPatchThreads = kPatchWarps * 32;
+constexpr int kFirstProducer = kSumWarps + kPatchWarps;
+// One producer a stage: a stage's phases then are one warp's to wait for, in
+// order.  (With more producers than stages one could wait two phases ahead, which
+// a parity cannot tell from the phase before.)
+template <int RING>
+constexpr int rule_threads() { return (kFirstProducer + RING) * 32; }
+constexpr int kListCap = 512;                        // touched ids of a warp kept as a list
 constexpr uint32_t kCountFull = 0xffffu;             // a count that no longer fits
 constexpr int64_t kNoSeq = INT64_MIN;
 constexpr int kMaxNew = 6;                           // new tokens of a row handed on one by one
 constexpr uint64_t kRuleWaitNs = 4000000000ull;      // 4 s: a copy, or the other warps
 constexpr uint64_t kRuleDrainNs = 1000000000ull;
 constexpr int kBlockIds = 32;
+constexpr int kMaskCache = 256;                      // masks whose size is remembered
 
 // What the producer tells about one row.
 struct __align__(16) RowDesc {
-    int32_t tok;                // the scored token, from the slice's start (or < 0, or past it)
+    int32_t tok;                // the scored token's local number, or -1
     int32_t bad;                // status bits so far
     int32_t flags;              // kDesc*
     int32_t n_new;
-    int32_t fresh[kMaxNew];     // new tokens from the slice's start, or -1; kMade set: generated
+    int32_t fresh[kMaxNew];     // new tokens' local numbers, -1 or kFreshBad; kMade set: generated
     int32_t pad[2];
 };
 constexpr int32_t kDescRebuild = 1, kDescMask = 2, kDescSparse = 4;
+// Narrow masks: copied by vectors while they would take at most this part of the
+// slice.  (A copy of 16 bytes takes a memory sector of its own, and time to issue;
+// bulk copies of 16 bytes would take more, as a warp issues them one by one.)
+constexpr int32_t kSparseShare = 16;
 constexpr int32_t kMade = 0x40000000;
+constexpr int32_t kFreshBad = 0x20000000;            // not an id of the vocabulary
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Shared memory of a block.  NB: blocks of 32 ids per lane; RING: stages.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes) : "memory");
+}
+
+// 16 bytes by the calling thread, asynchronously; and an arrival once its copies
+// so far have landed.
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Shared memory of a block.  NB: blocks of 32 ids per lane of the summing warps;
+// RING: stages.
 template <int DT, int NB, int RING>
 struct RuleSmem {
     static constexpr int kEsz = DT == PS_BF16 ? 2 : 4;
-    static constexpr int kIds = kRuleWarps * 32 * NB * kBlockIds;     // of a slice, at most
-    static constexpr int kWarpIds = kIds / kRuleWarps;
+    static constexpr int kIds = kSumWarps * 32 * NB * kBlockIds;      // of a slice, at most
+    static constexpr int kBlocks = kIds / kBlockIds;
     uint8_t stage[RING][kIds * kEsz];
-    uint32_t mask[RING][kIds / 32];
-    uint16_t count[kRuleWarps][kWarpIds];
-    uint32_t seen[kRuleWarps][kWarpIds / 32];
-    uint32_t biased[kRuleWarps][kWarpIds / 32];
-    uint16_t list[kRuleWarps][kListCap];             // ids from the slice's start
-    float list_bias[kRuleWarps][kListCap];
+    alignas(128) uint32_t mask[RING][kBlocks];
+    uint16_t count[kIds];
+    uint32_t seen[kBlocks];
+    uint32_t biased[kBlocks];
+    uint16_t list[kPatchWarps][kListCap];            // local numbers
+    float list_bias[kPatchWarps][kListCap];
     RowDesc desc[RING];
     RowRules rules[RING];
-    uint64_t full[RING], empty[RING], free[RING];
-    uint64_t sync;                                   // the consumers' own barrier
+    uint64_t mask_ids[kMaskCache];                   // a mask and slice, and its ids there
+    // a stage is full (producer and copies), patched, and read; free: may be filled
+    uint64_t full[RING], patched[RING], empty[RING], free[RING];
+    uint64_t sync;                                   // the patchers' own barrier
     int32_t bad[2];                                  // of a rebuild, by its parity
 };
 
-// Where id d of the slice belongs.
-__device__ __forceinline__ uint32_t owner_of(uint32_t d) {
-    const uint32_t b = d / kBlockIds, rem = b % 512;
-    return (rem - rem / 16) & 15u;
-}
-__device__ __forceinline__ uint32_t place_of(uint32_t d) {            // among the owner's ids
-    const uint32_t b = d / kBlockIds;
-    return ((b / 512) * 32 + (b % 512) / 16) * kBlockIds + d % kBlockIds;
-}
-// The lane's block h in the slice.
-__device__ __forceinline__ uint32_t block_of(int wid, int lane, int h) {
-    return h * 512 + lane * 16 + ((wid + lane) & 15);
-}
+__device__ __forceinline__ uint32_t owner_of(uint32_t d) { return (d / kBlockIds) % kPatchWarps; }
+
+// A slice of the vocabulary: its ids are numbered from 0 ("local").
+struct SliceMap {
+    int32_t V, n_slices, slice;
+    int32_t n_segs;             // segments of the slice
+    int32_t nid;                // ids of the slice
+    float inv;
+
+    __device__ SliceMap(const RuleCut &cut, int32_t V_, int32_t slice_)
+        : V(V_), n_slices(cut.n_slices), slice(slice_), inv(1.f / (float)cut.n_slices) {
+        n_segs = (cut.n_segs - slice + n_slices - 1) / n_slices;
+        const int32_t last = (n_segs - 1) * n_slices + slice;
+        nid = (n_segs - 1) * kSegIds + min(kSegIds, V - last * kSegIds);
+    }
+    // The local number of id v in [0, V); -1 if it is another slice's.  (The
+    // quotient of two numbers below 2^20 is off by one at most.)
+    __device__ __forceinline__ int32_t local(int32_t v) const {
+        const int32_t j = v / kSegIds;
+        int32_t q = (int32_t)((float)j * inv);
+        int32_t rem = j - q * n_slices;
+        if (rem < 0) rem += n_slices, --q;
+        if (rem >= n_slices) rem -= n_slices, ++q;
+        return rem == slice ? q * kSegIds + v % kSegIds : -1;
+    }
+    __device__ __forceinline__ int32_t global(int32_t d) const {
+        return ((d / kSegIds) * n_slices + slice) * kSegIds + d % kSegIds;
+    }
+};
 
 // Times that id is among tokens b .. e - 1.
 __device__ __noinline__ uint32_t recount(const int32_t *hist, int32_t b, int32_t e, int32_t id) {
@@ -114,7 +165,7 @@ struct RuleSpan {
     }
 };
 
-// The producer warp.  Sink: issues the copies of one row.
+// A producer warp: fills stage `me` with every RING-th row.
 // SPARSE: where a row's mask leaves few of the slice's ids, only the 16-byte
 // vectors that hold one are copied.
 template <int DT, int NB, int RING, bool SPARSE>
@@ -125,34 +176,32 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
                                               const int32_t *tokens, uint64_t *free_bars) {
     using Smem = RuleSmem<DT, NB, RING>;
     constexpr int kEsz = Smem::kEsz;
-    constexpr int kWords = Smem::kIds / 32;                // mask words of a slice
-    constexpr int kWpl = kWords / 32;                      // and of a lane
+    constexpr int kWpl = Smem::kBlocks / 32;               // mask words of a lane
+    constexpr int kVec = 16 / kEsz;                        // ids of a vector
+    static_assert(Smem::kIds / kSegIds <= 32, "a lane copies a segment");
     const ps_logit_rules &u = p.rules;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, me = (threadIdx.x >> 5) - kFirstProducer;
     const RuleSpan span(p.n_rows, cut.n_slices);
     const uint64_t policy = l2_evict_first_policy();
     const bool per_seq = u.seq_begin != nullptr || u.bias_begin != nullptr;
     const bool mask16 = u.mask && u.mask_ld % 4 == 0 && (reinterpret_cast<uintptr_t>(u.mask) & 15) == 0;
 
-    // entries of 32 rows, one a lane
+    // entries of rows base .. base + 31, one a lane
     int64_t base = -1;
     int32_t c_seq = 0, c_len = 0, c_mask = -1, c_tok = 0;
     int64_t c_src = 0;
-    // the sequence that the consumers know
-    int64_t seq = kNoSeq;
-    int32_t len = 0, win = 0, win_tok = 0, bad_hist = 0;
-    RowRules w{};
+    RowRules w{};                                          // of sequence w_seq
+    int64_t w_seq = kNoSeq;
+    int32_t win = -64, win_tok = 0;                        // 32 tokens of its history
 
-    int64_t r = span.t0 % span.rows;
-    int32_t slice = (int32_t)(span.t0 / span.rows);
-    uint32_t m[kWpl];                                      // the row's mask words, by lane
-    int s = 0;
-    uint32_t lap = 0;
-    int64_t t = span.t0;
-    for (; t < span.t1; ++t) {
-        if (base < 0 || r < base || r >= base + 32) {
-            base = r;
-            const int64_t i = r + lane;
+    int64_t t = span.t0 + me;
+    int64_t r = t % span.rows;
+    SliceMap map(cut, p.V, (int32_t)(t / span.rows));
+    for (; t < span.t1; t += RING) {
+        // the window holds r and the row before
+        if (base < 0 || r <= base || r >= base + 32) {
+            base = r > 0 ? r - 1 : 0;
+            const int64_t i = base + lane;
             const bool in = i < p.n_rows;
             c_seq = (in && per_seq && u.row_seq) ? __ldg(u.row_seq + i) : 0;
             c_len = (in && u.seq_begin && u.row_len) ? __ldg(u.row_len + i) : 0;
@@ -160,12 +209,11 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
             c_tok = (in && tokens) ? __ldg(tokens + i) : 0;
             c_src = (in && row_index) ? __ldg(row_index + i) : i;
         }
-        const int k = (int)(r - base);
-        const int32_t s0 = slice * cut.ids;
-        const int32_t nid = min(cut.ids, p.V - s0);        // ids of the slice
+        const int k = (int)(r - base), k0 = k > 0 ? k - 1 : 0;
         int32_t bad = 0, flags = 0;
-        const int64_t rm = u.row_mask ? (int64_t)__shfl_sync(0xffffffffu, c_mask, k) : r;
+        int64_t rm = -1;
         if (u.mask) {
+            rm = u.row_mask ? (int64_t)__shfl_sync(0xffffffffu, c_mask, k) : r;
             if (rm < (u.row_mask ? -1 : 0) || rm >= u.n_masks) bad |= PS_DEV_BAD_RULES;
             else if (rm >= 0) flags |= kDescMask;
         }
@@ -175,184 +223,187 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
             src = 0;
         }
         const int32_t tok = __shfl_sync(0xffffffffu, c_tok, k);
-        if (tokens && (tok < 0 || tok >= p.V)) bad |= PS_DEV_BAD_TOKEN;
+        int32_t tok_d = -1;
+        if (tokens) {
+            if (tok < 0 || tok >= p.V) bad |= PS_DEV_BAD_TOKEN;
+            else tok_d = map.local(tok);
+        }
 
+        // What changed since the row before.  Its sequence and length have to be
+        // in order, or the patchers do not know its history.
+        const bool by_row = per_seq && !u.row_seq;
+        const int64_t q = by_row ? r : (int64_t)__shfl_sync(0xffffffffu, c_seq, k);
+        const int64_t q0 = by_row ? r - 1 : (int64_t)__shfl_sync(0xffffffffu, c_seq, k0);
+        int32_t n = __shfl_sync(0xffffffffu, c_len, k), n0 = __shfl_sync(0xffffffffu, c_len, k0);
+        int32_t n_new = 0, fresh = -1;                     // fresh: by lane
+        if (q != w_seq) {
+            w = row_rules(p, r);
+            w_seq = w.bad ? kNoSeq : q;
+            win = -64;
+        }
+        if (!u.row_len || !u.seq_begin) n = n0 = w.len_all;
+        if (w_seq == q && q0 == q && t != span.t0 && r != 0 && n0 >= 0 && n0 <= w.len_all &&
+            n >= n0 && n <= w.len_all && n - n0 <= kMaxNew) {
+            n_new = n - n0;
+            if (n_new) {
+                if (n0 < win || n > win + 32) {
+                    win = n0;
+                    win_tok = win + lane < w.len_all ? __ldg(w.hist + win + lane) : 0;
+                }
+                const int32_t id = __shfl_sync(0xffffffffu, win_tok, (n0 - win + lane) & 31);
+                if (lane < n_new) {
+                    if (id < 0 || id >= p.V) fresh = kFreshBad;
+                    else fresh = map.local(id);
+                    if (fresh >= 0 && fresh != kFreshBad && n0 + lane >= w.prompt) fresh |= kMade;
+                }
+            }
+        } else {
+            w = row_rules(p, r);
+            w_seq = w.bad ? kNoSeq : q;
+            flags |= kDescRebuild;
+            bad |= w.bad;
+        }
+
+        const int64_t step = t - span.t0;
+        const int s = me;
+        const uint32_t lap = (uint32_t)(step / RING);
         if (lap > 0 && !mbar_wait_bounded(&free_bars[s], (lap - 1) & 1u, kRuleWaitNs)) {
             if (lane == 0) set_status(p.status, PS_DEV_TIMEOUT);
             break;
         }
         // logits and mask
-        const int64_t off = (int64_t)s0 * kEsz;
-        const uint32_t bytes = (uint32_t)min(((int64_t)nid * kEsz + 15) / 16 * 16, row_bytes - off);
-        const uint8_t *from = logits + src * ld_bytes + off;
-        int32_t left = 0;                                  // vectors that hold an allowed id
+        const uint32_t bytes = (uint32_t)(map.nid * kEsz + 15) / 16 * 16;
+        const uint8_t *from = logits + src * ld_bytes;
+        const uint32_t *mrow = u.mask + (flags & kDescMask ? rm * u.mask_ld : 0);
+        bool copy_mask = false;                            // by bulk copies too
         if (flags & kDescMask) {
-            const uint32_t *mrow = u.mask + rm * u.mask_ld + s0 / 32;
-            const int32_t nw = (nid + 31) / 32;
-            if (mask16) {
+            const uint64_t key = (uint64_t)(rm * cut.n_slices + map.slice) + 1;
+            uint64_t known = 0;
+            if (SPARSE) known = *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache];
+            copy_mask = mask16 && (!SPARSE || known >> 16 == key);
+            if (SPARSE && copy_mask && (int32_t)(known & 0xffffu) * 16 * kSparseShare <= (int32_t)bytes) {
+                flags |= kDescSparse;
+                copy_mask = false;
+            }
+            if (!copy_mask) {
+                uint32_t m[kWpl];                          // the slice's words, by lane
+                const int32_t nw = (map.nid + 31) / 32;
 #pragma unroll
                 for (int i = 0; i < kWpl; i += 4) {
                     const int at = i * 32 + lane * 4;
-                    uint4 q = make_uint4(0, 0, 0, 0);
-                    if (at < nw) q = __ldg(reinterpret_cast<const uint4 *>(mrow + at));
-                    m[i] = q.x;
-                    m[i + 1] = q.y;
-                    m[i + 2] = q.z;
-                    m[i + 3] = q.w;
-                    reinterpret_cast<uint4 *>(sm.mask[s])[at / 4] = q;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kWpl; ++i) {
-                    const int at = (i & ~3) * 32 + lane * 4 + (i & 3);
-                    m[i] = at < nw ? __ldg(mrow + at) : 0u;
-                    sm.mask[s][at] = m[i];
-                }
-            }
-            if constexpr (SPARSE) {
-#pragma unroll
-                for (int i = 0; i < kWpl; ++i) {
-                    const int at = (i & ~3) * 32 + lane * 4 + (i & 3);
-                    uint32_t x = m[i];
-                    if (at * 32 + 32 > nid) x &= at * 32 < nid ? (1u << (nid - at * 32)) - 1u : 0u;
-                    // one bit for each vector
-                    if constexpr (DT == PS_BF16) {
-                        x |= x >> 4;
-                        x |= x >> 2;
-                        x |= x >> 1;
-                        x &= 0x01010101u;
+                    const uint32_t *word = mrow + map.global(at * 32) / 32;
+                    if (mask16) {
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (at < nw) x = __ldg(reinterpret_cast<const uint4 *>(word));
+                        m[i] = x.x;
+                        m[i + 1] = x.y;
+                        m[i + 2] = x.z;
+                        m[i + 3] = x.w;
                     } else {
-                        x |= x >> 2;
-                        x |= x >> 1;
-                        x &= 0x11111111u;
-                    }
-                    m[i] = x;
-                    left += __popc(x);
-                }
-                left = __reduce_add_sync(0xffffffffu, left);
-                if (left * 16 * 8 <= (int32_t)bytes) flags |= kDescSparse;
-            }
-        }
-        if (lane == 0) {
-            fence_proxy_async_smem();
-            if (flags & kDescSparse) {
-                if (left) asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(
-                                           smem_addr(&sm.full[s])), "r"(left * 16) : "memory");
-            } else {
-                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(
-                                 smem_addr(&sm.full[s])), "r"(bytes) : "memory");
-                bulk_g2s(sm.stage[s], from, bytes, &sm.full[s], policy);
-            }
-        }
-        __syncwarp();
-        if (SPARSE && (flags & kDescSparse)) {
-            fence_proxy_async_smem();
 #pragma unroll
-            for (int i = 0; i < kWpl; ++i) {
-                const int at = (i & ~3) * 32 + lane * 4 + (i & 3);
-                for (uint32_t x = m[i]; x; x &= x - 1) {
-                    const uint32_t o = (uint32_t)(at * 32 + (__ffs(x) - 1)) * kEsz;   // of the vector
-                    bulk_g2s(sm.stage[s] + o, from + o, 16, &sm.full[s], policy);
-                }
-            }
-        }
-        // what changed since the row before
-        const int64_t q = per_seq && !u.row_seq ? r : (int64_t)__shfl_sync(0xffffffffu, c_seq, k);
-        int32_t n = __shfl_sync(0xffffffffu, c_len, k), n_new = 0;
-        bool again = true;
-        if (q == seq) {
-            if (!u.row_len || !u.seq_begin) n = len;
-            if (n > w.len_all) {                           // only this row is wrong
-                bad |= PS_DEV_BAD_RULES;
-                again = false;
-            } else if (n >= len && n - len <= kMaxNew) {
-                again = false;
-                n_new = n - len;
-                for (int j = 0; j < n_new; ++j, ++len) {
-                    if (len < win || len >= win + 32) {
-                        win = len;
-                        win_tok = win + lane < w.len_all ? __ldg(w.hist + win + lane) : 0;
+                        for (int j = 0; j < 4; ++j) m[i + j] = at + j < nw ? __ldg(word + j) : 0u;
                     }
-                    const int32_t id = __shfl_sync(0xffffffffu, win_tok, len - win);
-                    int32_t d = -1;
-                    if (id < 0 || id >= p.V) bad_hist |= PS_DEV_BAD_TOKEN;
-                    else if (id >= s0 && id - s0 < nid) d = (id - s0) | (len >= w.prompt ? kMade : 0);
-                    if (lane == 0) sm.desc[s].fresh[j] = d;
+                }
+                int32_t ids = 0;
+#pragma unroll
+                for (int i = 0; i < kWpl; i += 4) {
+                    reinterpret_cast<uint4 *>(sm.mask[s])[i * 8 + lane] =
+                        make_uint4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+                    ids += __popc(m[i]) + __popc(m[i + 1]) + __popc(m[i + 2]) + __popc(m[i + 3]);
+                }
+                if constexpr (SPARSE) {
+                    ids = __reduce_add_sync(0xffffffffu, ids);
+                    if (lane == 0) *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache] = key << 16 | ids;
+                    if (ids * 16 * kSparseShare <= (int32_t)bytes) {
+                        flags |= kDescSparse;
+                        fence_proxy_async_smem();
+#pragma unroll
+                        for (int i = 0; i < kWpl; ++i) {
+                            const int at = ((i & ~3) * 32 + lane * 4 + (i & 3)) * 32;
+                            uint32_t x = m[i];
+                            while (x) {
+                                // the vector that holds the lowest id left
+                                const int v = (__ffs(x) - 1) / kVec * kVec;
+                                const int32_t d = at + v;
+                                if (d < map.nid)
+                                    copy16(sm.stage[s] + d * kEsz,
+                                           from + (int64_t)map.global(d) * kEsz);
+                                x &= ~(((1u << kVec) - 1u) << v);
+                            }
+                        }
+                    }
                 }
             }
         }
-        if (again) {
-            w = row_rules(p, r);
-            // a row that fails a check says nothing about the next one
-            seq = w.bad ? kNoSeq : q;
-            len = w.len;
-            win = -64;
-            bad_hist = 0;
-            flags |= kDescRebuild;
-            if (lane == 0) sm.rules[s] = w;
+        if (!(flags & kDescSparse)) {
+            const uint32_t mask_bytes = copy_mask ? (uint32_t)((map.nid + 127) / 128 * 16) : 0u;
+            if (lane == 0) {
+                fence_proxy_async_smem();
+                mbar_expect_tx(&sm.full[s], bytes + mask_bytes);
+            }
+            __syncwarp();
+            if (lane < map.n_segs) {
+                const int64_t v = ((int64_t)lane * map.n_slices + map.slice) * kSegIds;
+                bulk_g2s(sm.stage[s] + lane * (kSegIds * kEsz), from + v * kEsz,
+                         (uint32_t)min((int64_t)(kSegIds * kEsz), row_bytes - v * kEsz), &sm.full[s],
+                         policy);
+                if (copy_mask)
+                    bulk_g2s(&sm.mask[s][lane * (kSegIds / 32)], mrow + v / 32,
+                             (uint32_t)min((int64_t)(kSegIds / 8), (p.V - v + 127) / 128 * 16),
+                             &sm.full[s], policy);
+            }
         }
+        RowDesc &d = sm.desc[s];
+        if (lane < n_new) d.fresh[lane] = fresh;
         if (lane == 0) {
-            RowDesc &d = sm.desc[s];
-            d.tok = tok - s0;
-            d.bad = bad | bad_hist | w.bad;
-            d.flags = flags;
-            d.n_new = n_new;
+            *reinterpret_cast<int4 *>(&d) = make_int4(tok_d, bad, flags, n_new);
+            if (flags & kDescRebuild) sm.rules[s] = w;
         }
+        // each lane's own copies (if any), then what the warp has written
+        arrive_after_copies(&sm.full[s]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.full[s]);
-        if (++s == RING) {
-            s = 0;
-            ++lap;
-        }
-        if (++r == span.rows) {
-            r = 0;
-            ++slice;
-            seq = kNoSeq;
+        for (r += RING; r >= span.rows; r -= span.rows) {
+            map = SliceMap(cut, p.V, map.slice + 1);
             base = -1;
         }
     }
     // copies in flight land before the block's memory goes
-    const int64_t issued = t - span.t0;
-    for (int64_t j = max(issued - RING, (int64_t)0); j < issued; ++j)
-        mbar_wait_bounded(&sm.full[j % RING], (uint32_t)(j / RING) & 1u, kRuleDrainNs);
+    t -= RING;                                             // the last row that was filled
+    if (t >= span.t0 && t < span.t1) {
+        const int64_t step = t - span.t0;
+        mbar_wait_bounded(&sm.full[me], (uint32_t)(step / RING) & 1u, kRuleDrainNs);
+    }
 }
 
-// A consumer warp's view of the rules.  The same in all lanes unless said
+// A patching warp's view of the rules.  The same in all lanes unless said
 // otherwise.
 template <typename Smem>
 struct RuleWalk {
     Smem &sm;
     const RulesParams &p;
-    const int lane, wid;
-    int32_t s0 = 0;             // first id of the slice
-    int32_t nid = 0;            // ids of the slice
+    const int lane, wid;        // wid: among the patchers
+    SliceMap map;
     int32_t len = 0;            // tokens of history that are counted
     int32_t n_list = 0;         // touched ids; the first n_bias of the list are biased
     int32_t n_bias = 0;
     int32_t bad = 0;            // status bits of the history and the biases
-    uint32_t lap = 0;           // of the consumers' own barrier: two a rebuild
+    uint32_t lap = 0;           // of the patchers' own barrier
+    uint32_t rebuilds = 0;
     RowRules w{};
     float inv_rho = 1.f;
     // by lane: entry `lane` of the list, -1 if there is none
     int32_t e_id = -1;
     float e_pos = 1.f, e_neg = 1.f, e_add = 0.f;
 
-    __device__ RuleWalk(Smem &sm_, const RulesParams &p_)
-        : sm(sm_), p(p_), lane(threadIdx.x & 31), wid(threadIdx.x >> 5) {}
+    __device__ RuleWalk(Smem &sm_, const RulesParams &p_, const SliceMap &map_)
+        : sm(sm_), p(p_), lane(threadIdx.x & 31), wid((threadIdx.x >> 5) - kSumWarps), map(map_) {}
 
-    __device__ __forceinline__ void enter_slice(int32_t slice, const RuleCut &cut) {
-        s0 = slice * cut.ids;
-        nid = min(cut.ids, p.V - s0);
-    }
-    __device__ __forceinline__ bool is_seen(uint32_t d) const {
-        const uint32_t o = place_of(d);
-        return (sm.seen[wid][o >> 5] >> (o & 31)) & 1u;
-    }
+    __device__ __forceinline__ bool is_seen(uint32_t d) const { return (sm.seen[d >> 5] >> (d & 31)) & 1u; }
     __device__ __forceinline__ bool is_biased(uint32_t d) const {
-        const uint32_t o = place_of(d);
-        return (sm.biased[wid][o >> 5] >> (o & 31)) & 1u;
+        return (sm.biased[d >> 5] >> (d & 31)) & 1u;
     }
-    // Waits for the other consumers; false when they do not come.
+    // Waits for the other patchers; false when they do not come.
     __device__ __forceinline__ bool meet() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.sync);
@@ -365,8 +416,8 @@ struct RuleWalk {
     // again from the history: slow, and as rare as a token that one sequence holds
     // 65535 times.
     __device__ __forceinline__ uint32_t times(uint32_t d) const {
-        const uint32_t c = sm.count[wid][place_of(d)];
-        return c == kCountFull ? recount(w.hist, max(0, w.prompt), len, s0 + (int32_t)d) : c;
+        const uint32_t c = sm.count[d];
+        return c == kCountFull ? recount(w.hist, max(0, w.prompt), len, map.global((int32_t)d)) : c;
     }
 
     // The processed logit of id d from its logit: a factor by sign, then a sum that
@@ -387,18 +438,17 @@ struct RuleWalk {
         }
     }
 
-    __device__ __forceinline__ void count_shared(int32_t i, int32_t id, bool fits) {
+    __device__ __forceinline__ void count_shared(int32_t i, int32_t id, bool fits, int32_t *bad_word) {
         if (id < 0 || id >= p.V) {
-            atomicOr(&sm.bad[(lap >> 1) & 1], PS_DEV_BAD_TOKEN);
+            atomicOr(bad_word, PS_DEV_BAD_TOKEN);
             return;
         }
-        const uint32_t d = (uint32_t)(id - s0);
-        if (d >= (uint32_t)nid) return;
-        const uint32_t q = owner_of(d), o = place_of(d);
-        atomicOr(&sm.seen[q][o >> 5], 1u << (o & 31));
+        const int32_t d = map.local(id);
+        if (d < 0) return;
+        atomicOr(&sm.seen[d >> 5], 1u << (d & 31));
         if (i < w.prompt) return;
-        uint32_t *word = reinterpret_cast<uint32_t *>(&sm.count[q][o & ~1u]);
-        const int sh = (o & 1) * 16;
+        uint32_t *word = reinterpret_cast<uint32_t *>(&sm.count[d & ~1u]);
+        const int sh = (d & 1) * 16;
         if (fits) {
             atomicAdd(word, 1u << sh);
         } else {
@@ -413,33 +463,41 @@ struct RuleWalk {
 
     // Takes up a row's sequence with its history so far.  False on a timeout.
     __device__ __forceinline__ bool rebuild(const RowRules &from) {
+        const int tid = threadIdx.x - kSumWarps * 32;
         w = from;
         inv_rho = 1.f / w.rho;
         len = w.len;
-        // the warp's own ids (blocks past the slice are never touched)
-        const int32_t blocks = (nid + kBlockIds - 1) / kBlockIds;
-        for (int h = 0; h * 512 < blocks; ++h) {
-            const int nl = min(32, (blocks - h * 512 + 15) / 16);      // lanes that own one
-            for (int i = lane; i < nl * kBlockIds / 8; i += 32)
-                reinterpret_cast<uint4 *>(sm.count[wid])[h * 128 + i] = make_uint4(0, 0, 0, 0);
-            sm.seen[wid][h * 32 + lane] = sm.biased[wid][h * 32 + lane] = 0;
-        }
+        const int32_t blocks = (map.nid + kBlockIds - 1) / kBlockIds;
         // a warp may still read the word of the rebuild before
-        int32_t *bad_word = &sm.bad[(lap >> 1) & 1];
-        if (threadIdx.x == 0) *bad_word = 0;
+        int32_t *bad_word = &sm.bad[rebuilds++ & 1];
+        if (tid == 0) *bad_word = 0;
+        if (!meet()) return false;                  // the others are done with the tables
+        for (int i = tid; i < blocks * kBlockIds / 8; i += kPatchThreads)
+            reinterpret_cast<uint4 *>(sm.count)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < blocks; i += kPatchThreads) sm.seen[i] = sm.biased[i] = 0;
         if (!meet()) return false;
         const bool fits = w.len - max(0, min(w.prompt, w.len)) < (int32_t)kCountFull;
-        for (int i = threadIdx.x; i < w.len; i += kRuleWarps * 32) count_shared(i, __ldg(w.hist + i), fits);
-        for (int i = threadIdx.x; i < w.n_bias; i += kRuleWarps * 32) {
+        for (int b = 0; b < w.len; b += kPatchThreads * 4) {
+            int32_t id[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = b + j * kPatchThreads + tid;
+                id[j] = i < w.len ? __ldg(w.hist + i) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = b + j * kPatchThreads + tid;
+                if (i < w.len) count_shared(i, id[j], fits, bad_word);
+            }
+        }
+        for (int i = tid; i < w.n_bias; i += kPatchThreads) {
             const int32_t id = __ldg(w.bias_ids + i);
             if (id < 0 || id >= p.V || (i > 0 && id <= __ldg(w.bias_ids + i - 1))) {
-                atomicOr(&sm.bad[(lap >> 1) & 1], PS_DEV_BAD_RULES);
+                atomicOr(bad_word, PS_DEV_BAD_RULES);
                 continue;
             }
-            const uint32_t d = (uint32_t)(id - s0);
-            if (d >= (uint32_t)nid) continue;
-            const uint32_t o = place_of(d);
-            atomicOr(&sm.biased[owner_of(d)][o >> 5], 1u << (o & 31));
+            const int32_t d = map.local(id);
+            if (d >= 0) atomicOr(&sm.biased[d >> 5], 1u << (d & 31));
         }
         if (!meet()) return false;
         bad = *reinterpret_cast<volatile int32_t *>(bad_word);
@@ -447,8 +505,8 @@ struct RuleWalk {
         n_list = 0;
         for (int b = 0; bad == 0 && b < w.n_bias; b += 32) {
             const int32_t id = b + lane < w.n_bias ? __ldg(w.bias_ids + b + lane) : -1;
-            const uint32_t d = (uint32_t)(id - s0);
-            const bool mine = id >= 0 && d < (uint32_t)nid && owner_of(d) == (uint32_t)wid;
+            const int32_t d = id >= 0 ? map.local(id) : -1;
+            const bool mine = d >= 0 && owner_of(d) == (uint32_t)wid;
             const uint32_t all = __ballot_sync(0xffffffffu, mine);
             const int32_t at = n_list + __popc(all & ((1u << lane) - 1u));
             if (mine && at < kListCap) {
@@ -458,8 +516,9 @@ struct RuleWalk {
             n_list += __popc(all);
         }
         n_bias = n_list;
-        for (int h = 0; h * 512 < blocks; ++h) {
-            uint32_t m = sm.seen[wid][h * 32 + lane] & ~sm.biased[wid][h * 32 + lane];
+        for (int b0 = 0; b0 < blocks; b0 += kPatchThreads) {
+            const int b = b0 + lane * kPatchWarps + wid;
+            uint32_t m = b < blocks ? sm.seen[b] & ~sm.biased[b] : 0u;
             int32_t at = __popc(m);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -469,8 +528,7 @@ struct RuleWalk {
             const int32_t total = __shfl_sync(0xffffffffu, at, 31);
             at += n_list - __popc(m);
             for (; m != 0; m &= m - 1, ++at)
-                if (at < kListCap)
-                    sm.list[wid][at] = (uint16_t)(block_of(wid, lane, h) * kBlockIds + __ffs(m) - 1);
+                if (at < kListCap) sm.list[wid][at] = (uint16_t)(b * kBlockIds + __ffs(m) - 1);
             n_list += total;
         }
         __syncwarp();
@@ -480,12 +538,12 @@ struct RuleWalk {
 
     // One more token, of the warp's own ids.
     __device__ __forceinline__ void insert(uint32_t d, bool made) {
-        const uint32_t o = place_of(d), c = sm.count[wid][o];
+        const uint32_t c = sm.count[d];
         const bool seen = is_seen(d), listed = !seen && !is_biased(d);
         __syncwarp();
         if (lane == 0) {
-            if (made && c != kCountFull) sm.count[wid][o] = (uint16_t)(c + 1);
-            if (!seen) sm.seen[wid][o >> 5] |= 1u << (o & 31);
+            if (made && c != kCountFull) sm.count[d] = (uint16_t)(c + 1);
+            if (!seen) sm.seen[d >> 5] |= 1u << (d & 31);
             if (listed && n_list < kListCap) sm.list[wid][n_list] = (uint16_t)d;
         }
         if (listed) ++n_list;
@@ -493,13 +551,14 @@ struct RuleWalk {
     }
 
     // Moves to the row of the stage.  False on a timeout.
-    __device__ __forceinline__ bool enter_row(int s, const RowDesc &d) {
-        if (d.flags & kDescRebuild) return rebuild(sm.rules[s]);
+    __device__ __forceinline__ bool enter_row(int s, int32_t flags, int32_t n_new) {
+        if (flags & kDescRebuild) return rebuild(sm.rules[s]);
         bool own = false;
-        for (int j = 0; j < d.n_new; ++j) {
+        for (int j = 0; j < n_new; ++j) {
             const int32_t x = sm.desc[s].fresh[j];
             ++len;
-            if (x < 0) continue;
+            if (x == kFreshBad) bad |= PS_DEV_BAD_TOKEN;
+            if (x < 0 || x == kFreshBad) continue;
             const uint32_t id = (uint32_t)(x & ~kMade);
             if (owner_of(id) != (uint32_t)wid) continue;
             insert(id, (x & kMade) != 0);
@@ -522,14 +581,14 @@ struct RuleWalk {
                   summand(d, i < n_bias ? sm.list_bias[wid][i] : 0.f));
             }
         } else {
-            for (int h = 0; h * 512 * kBlockIds < nid; ++h) {
-                const uint32_t sw = sm.seen[wid][h * 32 + lane], bw = sm.biased[wid][h * 32 + lane];
+            for (int b = lane * kPatchWarps + wid; b * kBlockIds < map.nid; b += kPatchThreads) {
+                const uint32_t sw = sm.seen[b], bw = sm.biased[b];
                 for (uint32_t m = sw | bw; m != 0; m &= m - 1) {
-                    const int b = __ffs(m) - 1;
-                    const uint32_t d = block_of(wid, lane, h) * kBlockIds + b;
-                    const bool seen = (sw >> b) & 1u;
-                    const float bias = (bw >> b) & 1u ? bias_of(w.bias_ids, w.bias_values, w.n_bias,
-                                                                s0 + (int32_t)d) : 0.f;
+                    const int j = __ffs(m) - 1;
+                    const uint32_t d = b * kBlockIds + j;
+                    const bool seen = (sw >> j) & 1u;
+                    const float bias = (bw >> j) & 1u ? bias_of(w.bias_ids, w.bias_values, w.n_bias,
+                                                                map.global((int32_t)d)) : 0.f;
                     f(d, seen ? inv_rho : 1.f, seen ? w.rho : 1.f, summand(d, bias));
                 }
             }
@@ -539,13 +598,15 @@ struct RuleWalk {
 
 template <typename Smem, int RING>
 __device__ __forceinline__ void rule_smem_init(Smem &sm, int free_count) {
+    for (int i = threadIdx.x; i < kMaskCache; i += blockDim.x) sm.mask_ids[i] = 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < RING; ++s) {
-            mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], kRuleWarps);
+            mbar_init(&sm.full[s], 33);               // the producer's lanes, and once more
+            mbar_init(&sm.patched[s], kPatchWarps);
+            mbar_init(&sm.empty[s], kSumWarps);
             mbar_init(&sm.free[s], free_count);
         }
-        mbar_init(&sm.sync, kRuleWarps);
+        mbar_init(&sm.sync, kPatchWarps);
         fence_mbar_init();
     }
 }

@@ -22,15 +22,17 @@ struct ProcessParams {
     int32_t n_slices;
 };
 
-// How the vocabulary is cut for the kernels that stream rows.
+// How the vocabulary is cut for the kernels that stream rows: into segments of
+// kSegIds ids, dealt to the slices in turn.
+constexpr int32_t kSegIds = 2048;
 struct RuleCut {
-    int32_t ids;                // of a slice, a multiple of 128
+    int32_t n_segs;
     int32_t n_slices;
 };
-// most: ids of a slice at most (a multiple of 128).
+// most: ids of a slice at most (a multiple of kSegIds).
 RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows);
 RuleCut score_cut(int32_t V, int32_t dtype, int64_t n_rows);
-constexpr int kScoreParts = 16;     // partial sums of a slice of a row
+constexpr int kScoreParts = 16;     // partial sums of a slice of a row: one a warp
 
 // Sums of one warp's ids of a slice (ps_row_sums.cuh has their meaning).
 struct __align__(16) ChunkPart {
@@ -57,7 +59,7 @@ namespace {
 
 constexpr int kSliceIds = 8192;
 constexpr uint32_t kSeen = 0x80000000u;      // count word: the id was seen
-constexpr int kRuleThreads = 256;
+constexpr int kTableThreads = 256;
 
 // What row r's rules are, read and checked.
 struct RowRules {
@@ -126,13 +128,13 @@ __device__ __forceinline__ RowRules row_rules(const RulesParams &p, int64_t r) {
 struct SliceTable {
     uint32_t count[kSliceIds];         // times generated, and kSeen
     uint32_t biased[kSliceIds / 32];   // bit: in the sequence's bias list
-    // Bit b of word w: id v0 + w + kRuleThreads b was seen.  Thread w takes word
+    // Bit b of word w: id v0 + w + kTableThreads b was seen.  Thread w takes word
     // w's ids, so which thread takes an id does not depend on timing (a list in
     // order of arrival would change the order of float sums), and neighbouring
     // ids, which common tokens often are, go to different threads.
-    uint32_t seen[kRuleThreads];
+    uint32_t seen[kTableThreads];
 };
-static_assert(kSliceIds == 32 * kRuleThreads, "one word of seen ids per thread");
+static_assert(kSliceIds == 32 * kTableThreads, "one word of seen ids per thread");
 
 // Fills `t` for one row; ends with a barrier.  Returns the status bits of the
 // whole history and bias list (the same in every thread).
@@ -153,7 +155,7 @@ __device__ int32_t build_table(SliceTable &t, const RowRules &w, int32_t V, int3
         const uint32_t o = (uint32_t)(id - v0);
         if (o >= (uint32_t)kSliceIds) continue;
         atomicOr(&t.count[o], kSeen);
-        atomicOr(&t.seen[o % kRuleThreads], 1u << (o / kRuleThreads));
+        atomicOr(&t.seen[o % kTableThreads], 1u << (o / kTableThreads));
         if (i >= w.prompt) atomicAdd(&t.count[o], 1u);
     }
     for (int i = tid; i < w.n_bias; i += blockDim.x) {
@@ -174,7 +176,7 @@ __device__ int32_t build_table(SliceTable &t, const RowRules &w, int32_t V, int3
 template <typename F>
 __device__ __forceinline__ void for_seen(const SliceTable &t, F f) {
     for (uint32_t w = t.seen[threadIdx.x]; w != 0; w &= w - 1)
-        f(threadIdx.x + kRuleThreads * (uint32_t)(__ffs(w) - 1));
+        f(threadIdx.x + kTableThreads * (uint32_t)(__ffs(w) - 1));
 }
 
 __device__ __forceinline__ bool is_biased(const SliceTable &t, uint32_t o) {

@@ -2,13 +2,14 @@
 // (ps_score_rows_rules), without writing the processed rows.
 //
 // The formulation is ps_score_rows.cu's: sums relative to a reference, the token
-// left out.  ps_rule_rows.cuh brings the rows to the consumer warps.  In the
-// stage a warp takes the token and the ids that penalties or biases touch out
-// (their places become -inf) and adds their processed float32 values on their
-// own, so nothing is rounded to the rows' type.  It then reads its ids into
-// registers, gives the stage back, applies the mask and sums.  What is left are 16
-// partial sums for each slice of a row, which a second kernel joins in their
-// order.
+// left out.  ps_rule_rows.cuh brings the rows to the block.  Its patchers take the
+// token and the ids that penalties or biases touch out of the stage (their places
+// become -inf) and sum their processed float32 values on their own, so nothing is
+// rounded to the rows' type.  Each of the other 12 warps reads its ids into
+// registers, gives the stage back, applies the mask and sums: lane l of warp w has
+// blocks of 32 ids 12 (32 h + l) + (w + l) % 12, where the skew puts the lanes'
+// vectors in different banks.  What is left are 16 partial sums for each slice of a
+// row, which a second kernel joins in their order.
 //
 // Where a mask leaves a lane at most kFewIds of its 64 (32 for float32) ids, the
 // warp steps through the allowed ones instead of exponentiating all; where it
@@ -23,13 +24,14 @@
 namespace ps {
 namespace {
 
-constexpr int kRing = 2;
+constexpr int kRing = 3;
 constexpr int kFewIds = 10;
 constexpr float kLeast = 8.673617379884035e-19f;     // 2^-60
 
 template <int DT>
 struct ScoreSmem : RuleSmem<DT, DT == PS_BF16 ? 2 : 1, kRing> {
     uint4 lut[DT == PS_BF16 ? 256 : 16];             // mask bits -> which words stay
+    uint4 off[8];                                    // a block that does not count
 };
 
 __device__ __forceinline__ float warp_max_nan(float m) {
@@ -52,6 +54,11 @@ __device__ __forceinline__ float tau_term(float y, float e, float g) {
     else if constexpr (NP == 2) return e * e;
     else if constexpr (NP == 4) return (e * e) * (e * e);
     else return ((e * e) * (e * e)) * ((e * e) * (e * e));
+}
+
+// The lane's block h in the slice.
+__device__ __forceinline__ uint32_t block_of(int wid, int lane, int h) {
+    return (h * 32 + lane) * kSumWarps + (wid + lane) % kSumWarps;
 }
 
 // Sums relative to a reference, by lane.
@@ -152,15 +159,112 @@ __device__ __forceinline__ void raise_floor(uint4 (&q)[8]) {
     }
 }
 
+// The patchers' rows: takes the token and the touched ids out of each stage and
+// leaves their sums as partial sums of their own.
+template <int DT, int NP, bool ENT, typename Smem>
+__device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) {
+    constexpr uint32_t kOff = ENT ? Elem<DT>::kFloorWord : Elem<DT>::kNegInfWord;
+    const int lane = threadIdx.x & 31;
+    const float g = p.rows.g;
+    const RuleSpan span(p.r.n_rows, p.cut.n_slices);
+    int64_t r = span.t0 % span.rows;
+    RuleWalk<Smem> walk(sm, p.r, SliceMap(p.cut, p.r.V, (int32_t)(span.t0 / span.rows)));
+    int s = 0;
+    uint32_t lap = 0;
+    for (int64_t t = span.t0; t < span.t1; ++t) {
+        if (!mbar_wait_bounded(&sm.full[s], lap & 1u, kRuleWaitNs)) {
+            if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
+            return;
+        }
+        uint8_t *buf = sm.stage[s];
+        const int4 dh = *reinterpret_cast<const int4 *>(&sm.desc[s]);       // tok, bad, flags, n_new
+        if (((dh.z & kDescRebuild) || dh.w) && !walk.enter_row(s, dh.z, dh.w)) {
+            if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
+            return;
+        }
+        const int32_t bad = dh.y | walk.bad;
+        const int32_t tok = dh.x;
+        const uint32_t *mw = dh.z & kDescMask ? sm.mask[s] : nullptr;
+        if (walk.map.slice == 0 && walk.wid == 0 && lane == 0) {
+            if (bad) set_status(p.r.status, bad);
+            p.row_bad[r] = bad;
+        }
+        float px = -INFINITY;                         // a touched id of this lane, and
+        Acc more = acc_empty();                       // its others
+        auto put_off = [&](uint32_t d) {
+            if constexpr (DT == PS_BF16) reinterpret_cast<uint16_t *>(buf)[d] = (uint16_t)kOff;
+            else reinterpret_cast<uint32_t *>(buf)[d] = kOff;
+        };
+        auto allowed = [&](uint32_t d) { return mw == nullptr || ((mw[d >> 5] >> (d & 31)) & 1u); };
+        if (!bad) {
+            walk.for_touched([&](uint32_t d, float pos, float neg, float add) {
+                float l = load_elem<DT>(buf, d);
+                put_off(d);
+                l = fmaf(l, l > 0.f ? pos : neg, add);
+                if (!allowed(d)) l = -INFINITY;
+                if ((int32_t)d == tok) {
+                    p.tok_logit[r] = l;
+                } else if (px == -INFINITY) {
+                    px = l;
+                } else if (l != -INFINITY) {
+                    const float x = l * kLog2e;
+                    if (!(x <= more.R)) more = rebase<NP, ENT>(more, x, g);       // keeps a NaN
+                    const float y = x - more.R, e = ex2(y);
+                    more.s1 += e;
+                    more.st[0] += tau_term<NP>(y, e, g);
+                    more.y1 = fmaf(e, y, more.y1);
+                }
+            });
+            if (tok >= 0 && owner_of(tok) == (uint32_t)walk.wid &&
+                !walk.is_seen(tok) && !walk.is_biased(tok) && lane == 0) {
+                p.tok_logit[r] = allowed(tok) ? load_elem<DT>(buf, tok) : -INFINITY;
+                put_off(tok);
+            }
+        }
+        // ids past the vocabulary in the last block
+        if ((walk.map.nid & 31) && walk.wid == 0 && lane >= (walk.map.nid & 31))
+            put_off((uint32_t)(walk.map.nid & ~31) + lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.patched[s]);
+
+        ChunkPart part{-INFINITY, 0.f, 0.f, 0.f};
+        float m = max_nan_f32(px, more.R == more.R ? more.R * kLn2f : px);
+        m = warp_max_nan(m);
+        if (m != -INFINITY) {
+            const float ref = m * kLog2e;
+            Sums a{0.f, 0.f, 0.f};
+            if (px != -INFINITY) add_term<NP, ENT>(a, px * kLog2e - ref, g);
+            if (more.R != -INFINITY) {
+                const float d = more.R - ref, f = ex2(d);
+                a.s1 = fmaf(more.s1, f, a.s1);
+                if constexpr (NP != 1) a.st = fmaf(more.st[0], tau_term<NP>(d, f, g), a.st);
+                if constexpr (ENT) a.y1 += f * fmaf(d, more.s1, more.y1);
+            }
+            part.R = ref;
+            part.s1 = warp_sum(a.s1);
+            part.st = NP == 1 ? part.s1 : warp_sum(a.st);
+            if constexpr (ENT) part.y1 = warp_sum(a.y1);
+        }
+        if (lane == 0) p.parts[(r * p.cut.n_slices + walk.map.slice) * kScoreParts + kSumWarps + walk.wid] = part;
+        if (++s == kRing) {
+            s = 0;
+            ++lap;
+        }
+        if (++r == span.rows) {
+            r = 0;
+            walk.map = SliceMap(p.cut, p.r.V, walk.map.slice + 1);
+        }
+    }
+}
+
 template <int DT, int NP, bool ENT>
-__global__ void __launch_bounds__(kRuleWarps * 32 + 32, 1) score_rules_kernel(
+__global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
     const __grid_constant__ ScoreRulesParams p) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     using Smem = ScoreSmem<DT>;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     constexpr int kNb = DT == PS_BF16 ? 2 : 1;
-    constexpr int kEsz = Smem::kEsz;
-    constexpr int kVec = 16 / kEsz;                  // ids of a 16-byte vector
+    constexpr int kVec = 16 / Smem::kEsz;            // ids of a 16-byte vector
     constexpr int kBv = kBlockIds / kVec;            // vectors of a block: 4 or 8
     // the places of ids that do not count: -inf, or with entropy a large negative
     // value, which keeps 2^y y finite
@@ -179,112 +283,53 @@ __global__ void __launch_bounds__(kRuleWarps * 32 + 32, 1) score_rules_kernel(
         }
         sm.lut[i] = make_uint4(k[0], k[1], k[2], k[3]);
     }
+    if (threadIdx.x < kBv) sm.off[threadIdx.x] = make_uint4(kOff, kOff, kOff, kOff);
     rule_smem_init<Smem, kRing>(sm, 1);
     __syncthreads();
 
-    if (wid == kRuleWarps) {
+    if (wid >= kFirstProducer) {
         rule_producer<DT, kNb, kRing, true>(sm, p.r, p.cut, p.rows.logits, p.rows.ld_bytes,
                                             p.rows.row_bytes, p.rows.row_index, p.rows.n_logit_rows,
                                             p.rows.tokens, sm.empty);
         return;
     }
+    if (wid >= kSumWarps) {
+        patch_rows<DT, NP, ENT>(sm, p);
+        return;
+    }
 
     const RuleSpan span(p.r.n_rows, p.cut.n_slices);
-    RuleWalk<Smem> walk(sm, p.r);
     int64_t r = span.t0 % span.rows;
     int32_t slice = (int32_t)(span.t0 / span.rows);
-    walk.enter_slice(slice, p.cut);
+    int32_t nid = SliceMap(p.cut, p.r.V, slice).nid;
     float ref = 0.f;                                  // the warp's reference
     int s = 0;
     uint32_t lap = 0;
+    ChunkPart *part = p.parts + (r * p.cut.n_slices + slice) * kScoreParts + wid;
+    const uint32_t first = block_of(wid, lane, 0);
     for (int64_t t = span.t0; t < span.t1; ++t) {
-        if (!mbar_wait_bounded(&sm.full[s], lap & 1u, kRuleWaitNs)) {
+        if (!mbar_wait_bounded(&sm.full[s], lap & 1u, kRuleWaitNs) ||
+            !mbar_wait_bounded(&sm.patched[s], lap & 1u, kRuleWaitNs)) {
             if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
             return;
         }
-        uint8_t *buf = sm.stage[s];
-        const RowDesc &desc = sm.desc[s];
-        const int4 dh = *reinterpret_cast<const int4 *>(&desc);       // tok, bad, flags, n_new
-        if ((dh.z & kDescRebuild) || dh.w) {
-            if (!walk.enter_row(s, desc)) {
-                if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
-                return;
-            }
-        }
-        const int32_t bad = dh.y | walk.bad;
-        const int32_t tok = dh.x;
-        const bool masked = dh.z & kDescMask;
-        const uint32_t *mw = sm.mask[s];
-        if (walk.s0 == 0 && wid == 0 && lane == 0) {
-            if (bad) set_status(p.r.status, bad);
-            p.row_bad[r] = bad;
-        }
-        float px = -INFINITY;                         // a touched id of this lane, and
-        Acc more = acc_empty();                       // its others
-        auto put_off = [&](uint32_t d) {
-            if constexpr (DT == PS_BF16) reinterpret_cast<uint16_t *>(buf)[d] = (uint16_t)kOff;
-            else reinterpret_cast<uint32_t *>(buf)[d] = kOff;
-        };
-        if (!bad) {
-            walk.for_touched([&](uint32_t d, float pos, float neg, float add) {
-                float l = load_elem<DT>(buf, d);
-                put_off(d);
-                l = fmaf(l, l > 0.f ? pos : neg, add);
-                if (masked && !((mw[d >> 5] >> (d & 31)) & 1u)) l = -INFINITY;
-                if ((int32_t)d == tok) {
-                    p.tok_logit[r] = l;
-                } else if (px == -INFINITY) {
-                    px = l;
-                } else if (l != -INFINITY) {
-                    const float x = l * kLog2e;
-                    if (!(x <= more.R)) more = rebase<NP, ENT>(more, x, g);       // keeps a NaN
-                    const float y = x - more.R, e = ex2(y);
-                    more.s1 += e;
-                    more.st[0] += tau_term<NP>(y, e, g);
-                    more.y1 = fmaf(e, y, more.y1);
-                }
-            });
-            if ((uint32_t)tok < (uint32_t)walk.nid && owner_of(tok) == (uint32_t)wid &&
-                !walk.is_seen(tok) && !walk.is_biased(tok) && lane == 0) {
-                p.tok_logit[r] = masked && !((mw[tok >> 5] >> (tok & 31)) & 1u)
-                                     ? -INFINITY : load_elem<DT>(buf, tok);
-                put_off(tok);
-            }
-        }
-        // ids past the vocabulary in the last block
-        if (walk.nid & 31) {
-            const uint32_t d = (uint32_t)(walk.nid & ~31) + lane;
-            if (lane >= (walk.nid & 31) && owner_of(d) == (uint32_t)wid) put_off(d);
-        }
-        __syncwarp();
-
+        const uint8_t *buf = sm.stage[s];
+        const bool masked = sm.desc[s].flags & kDescMask;
         uint32_t m[kNb];
-        int few = 0;
+        int few = kFewIds + 1;
 #pragma unroll
-        for (int h = 0; h < kNb; ++h) {
-            const uint32_t b = block_of(wid, lane, h);
-            m[h] = b * kBlockIds < (uint32_t)walk.nid ? (masked ? mw[b] : 0xffffffffu) : 0u;
-            few += __popc(m[h]);
-        }
-        if (masked) few = __reduce_max_sync(0xffffffffu, few);
-        Sums sum{0.f, 0.f, 0.f};
-        const bool touched = __any_sync(0xffffffffu, px != -INFINITY);
-        // the touched ids' part relative to ref
-        auto add_touched = [&](Sums &a) {
-            if (px != -INFINITY) add_term<NP, ENT>(a, px * kLog2e - ref, g);
-            if (more.R != -INFINITY) {
-                const float d = more.R - ref, f = ex2(d);
-                a.s1 = fmaf(more.s1, f, a.s1);
-                if constexpr (NP != 1) a.st = fmaf(more.st[0], tau_term<NP>(d, f, g), a.st);
-                if constexpr (ENT) a.y1 += f * fmaf(d, more.s1, more.y1);
+        for (int h = 0; h < kNb; ++h) m[h] = (first + h * 32 * kSumWarps) * kBlockIds < (uint32_t)nid ? 0xffffffffu : 0u;
+        if (masked) {
+            few = 0;
+#pragma unroll
+            for (int h = 0; h < kNb; ++h) {
+                if (m[h]) m[h] = sm.mask[s][first + h * 32 * kSumWarps];
+                few += __popc(m[h]);
             }
-        };
-        auto touched_max = [&](float x) {
-            x = max_nan_f32(x, px);
-            if (more.R == more.R) x = max_nan_f32(x, more.R * kLn2f);
-            return x;
-        };
-        auto join_lanes = [&](Sums a) {
+            few = __reduce_max_sync(0xffffffffu, few);
+        }
+        Sums sum{0.f, 0.f, 0.f};
+        auto join_lanes = [&](const Sums &a) {
             sum.s1 = warp_sum(a.s1);
             sum.st = NP == 1 ? sum.s1 : warp_sum(a.st);
             if constexpr (ENT) sum.y1 = warp_sum(a.y1);
@@ -292,40 +337,33 @@ __global__ void __launch_bounds__(kRuleWarps * 32 + 32, 1) score_rules_kernel(
         auto in_range = [&]() {
             return sum.s1 >= kLeast && sum.s1 <= kLimit && sum.st >= kLeast && sum.st <= kLimit;
         };
-        if (masked && few <= kFewIds) {
-            if (few > 0 || touched) {
-                // step through the allowed ids of the lane
-                auto each = [&](auto f) {
+        if (few <= kFewIds) {
+            // step through the allowed ids of the lane
+            auto each = [&](auto f) {
 #pragma unroll
-                    for (int h = 0; h < kNb; ++h) {
-                        const uint32_t d0 = block_of(wid, lane, h) * kBlockIds;
-                        for (uint32_t x = m[h]; x != 0; x &= x - 1)
-                            f(load_elem<DT>(buf, d0 + __ffs(x) - 1));
+                for (int h = 0; h < kNb; ++h)
+                    for (uint32_t x = m[h]; x != 0; x &= x - 1)
+                        f(load_elem<DT>(buf, (first + h * 32 * kSumWarps) * kBlockIds + __ffs(x) - 1));
+            };
+            for (bool look = ENT; few > 0;) {
+                if (look) {
+                    float x = -INFINITY;
+                    each([&](float l) { x = max_nan_f32(x, l); });
+                    if (x <= kAbsentBelow) x = -INFINITY;
+                    x = warp_max_nan(x);
+                    if (x == -INFINITY) {
+                        sum = Sums{0.f, 0.f, 0.f};
+                        break;
                     }
-                };
-                for (bool look = ENT;;) {
-                    if (look) {
-                        float x = -INFINITY;
-                        each([&](float l) { x = max_nan_f32(x, l); });
-                        if (x <= kAbsentBelow) x = -INFINITY;
-                        x = warp_max_nan(touched_max(x));
-                        if (x == -INFINITY) {
-                            sum = Sums{0.f, 0.f, 0.f};
-                            break;
-                        }
-                        ref = x * kLog2e;
-                    }
-                    Sums a{0.f, 0.f, 0.f};
-                    each([&](float l) {
-                        const float y = fmaf(l, kLog2e, -ref);
-                        if (!(l <= kAbsentBelow)) add_term<NP, ENT>(a, y, g);
-                    });
-                    if constexpr (NP == 1) a.st = a.s1;
-                    add_touched(a);
-                    join_lanes(a);
-                    if (look || in_range()) break;
-                    look = true;
+                    ref = x * kLog2e;
                 }
+                Sums a{0.f, 0.f, 0.f};
+                each([&](float l) {
+                    if (!(l <= kAbsentBelow)) add_term<NP, ENT>(a, fmaf(l, kLog2e, -ref), g);
+                });
+                join_lanes(a);
+                if (look || in_range()) break;
+                look = true;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.empty[s]);
@@ -333,13 +371,11 @@ __global__ void __launch_bounds__(kRuleWarps * 32 + 32, 1) score_rules_kernel(
             uint4 q[8];
 #pragma unroll
             for (int h = 0; h < kNb; ++h) {
-                const uint4 *v = reinterpret_cast<const uint4 *>(buf) + block_of(wid, lane, h) * kBv;
+                const uint4 *v = m[h] ? reinterpret_cast<const uint4 *>(buf) + (first + h * 32 * kSumWarps) * kBv
+                                      : sm.off;
 #pragma unroll
-                for (int i = 0; i < kBv; ++i) {
-                    // the lanes' vectors in an order that spreads them over the banks
-                    const int at = kBv == 4 ? ((i + (lane >> 1)) & 3) : ((i + lane) & 7);
-                    q[h * kBv + i] = m[h] ? v[at] : make_uint4(kOff, kOff, kOff, kOff);
-                }
+                for (int i = 0; i < kBv; ++i)         // in an order that spreads over the banks
+                    q[h * kBv + i] = v[kBv == 4 ? ((i + (lane >> 1)) & 3) : ((i + lane) & 7)];
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.empty[s]);     // the stage is free
@@ -347,8 +383,8 @@ __global__ void __launch_bounds__(kRuleWarps * 32 + 32, 1) score_rules_kernel(
 #pragma unroll
                 for (int h = 0; h < kNb; ++h) {
                     // bits of vector i of the lane's order at the bottom of x
-                    uint32_t x = kBv == 4 ? __funnelshift_r(m[h], m[h], 8 * ((lane >> 1) & 3))
-                                          : __funnelshift_r(m[h], m[h], 4 * (lane & 7));
+                    const uint32_t x = kBv == 4 ? __funnelshift_r(m[h], m[h], 8 * ((lane >> 1) & 3))
+                                                : __funnelshift_r(m[h], m[h], 4 * (lane & 7));
 #pragma unroll
                     for (int i = 0; i < kBv; ++i) {
                         const uint4 k = sm.lut[kBv == 4 ? (x >> (8 * i)) & 0xffu : (x >> (4 * i)) & 15u];
@@ -360,45 +396,35 @@ __global__ void __launch_bounds__(kRuleWarps * 32 + 32, 1) score_rules_kernel(
                     }
                 }
             }
-            for (bool look = ENT;;) {
+            // 0: with the reference at hand; 1: with the maximum; 2: with the maximum,
+            // and -inf raised (among the logits it makes 2^y y NaN)
+            for (int look = ENT;; ++look) {
+                if (look == 2) raise_floor<DT>(q);
                 if (look) {
                     float x = max_of<DT>(q);
                     if (x <= kAbsentBelow) x = -INFINITY;
-                    x = warp_max_nan(touched_max(x));
+                    x = warp_max_nan(x);
                     if (x == -INFINITY) {             // nothing here
                         sum = Sums{0.f, 0.f, 0.f};
                         break;
                     }
                     ref = x * kLog2e;
                 }
-                Sums a = sum_dense<DT, NP, ENT>(q, ref, g);
-                add_touched(a);
-                if constexpr (NP == 1) a.st = a.s1;
-                join_lanes(a);
-                if constexpr (ENT) {
-                    // a -inf among the logits makes 2^y y NaN: raise it and sum again
-                    if (!(sum.y1 == sum.y1) && sum.s1 == sum.s1) {
-                        raise_floor<DT>(q);
-                        a = sum_dense<DT, NP, ENT>(q, ref, g);
-                        add_touched(a);
-                        if constexpr (NP == 1) a.st = a.s1;
-                        join_lanes(a);
-                    }
-                }
-                if (look || in_range()) break;
-                look = true;
+                join_lanes(sum_dense<DT, NP, ENT>(q, ref, g));
+                if (ENT ? look == 2 || sum.y1 == sum.y1 || sum.s1 != sum.s1 : look || in_range()) break;
             }
         }
-        if (lane == 0)
-            p.parts[(r * p.cut.n_slices + slice) * kScoreParts + wid] =
-                ChunkPart{sum.s1 == 0.f ? -INFINITY : ref, sum.s1, sum.st, sum.y1};
+        if (lane == 0) *part = ChunkPart{sum.s1 == 0.f ? -INFINITY : ref, sum.s1, sum.st, sum.y1};
+        part += p.cut.n_slices * kScoreParts;
         if (++s == kRing) {
             s = 0;
             ++lap;
         }
         if (++r == span.rows) {
             r = 0;
-            walk.enter_slice(++slice, p.cut);
+            ++slice;
+            if (slice < p.cut.n_slices) nid = SliceMap(p.cut, p.r.V, slice).nid;
+            part = p.parts + slice * kScoreParts + wid;
         }
     }
 }
@@ -430,7 +456,7 @@ cudaError_t launch(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int64_t tasks = p.r.n_rows * p.cut.n_slices;
     score_rules_kernel<DT, NP, ENT>
-        <<<(int)(tasks < sms ? tasks : sms), kRuleWarps * 32 + 32, smem, stream>>>(p);
+        <<<(int)(tasks < sms ? tasks : sms), rule_threads<kRing>(), smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     score_rules_join_kernel<NP, ENT><<<(unsigned)((p.r.n_rows + 7) / 8), 256, 0, stream>>>(p);
@@ -451,16 +477,15 @@ cudaError_t launch_np(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
 }  // namespace
 
 // As few slices as hold the vocabulary, or where there are few rows as many as
-// give every SM a block (of 1024 ids at least); all of the same size but the last.
+// give every SM a block (of a segment at least).
 RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows) {
     constexpr int64_t kBlocks = 152;
-    const int64_t least = ((int64_t)V + most - 1) / most;
-    const int64_t more = kBlocks / (n_rows > 0 ? n_rows : 1), fine = V / 1024;
-    int64_t slices = more < fine ? more : fine;
-    if (slices < least) slices = least;
     RuleCut c;
-    c.ids = (int32_t)(((V + slices - 1) / slices + 127) / 128 * 128);
-    c.n_slices = (int32_t)(((int64_t)V + c.ids - 1) / c.ids);
+    c.n_segs = (int32_t)(((int64_t)V + kSegIds - 1) / kSegIds);
+    const int64_t per = most / kSegIds, least = (c.n_segs + per - 1) / per;
+    int64_t slices = kBlocks / (n_rows > 0 ? n_rows : 1);
+    if (slices > c.n_segs) slices = c.n_segs;
+    c.n_slices = (int32_t)(slices > least ? slices : least);
     return c;
 }
 
