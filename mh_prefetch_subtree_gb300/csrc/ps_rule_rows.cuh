@@ -3,7 +3,7 @@
 //
 // A block owns a slice of the vocabulary and walks down the rows, so that
 // consecutive positions of a sequence, which differ by one token of history,
-// reuse what is known about the row before.  A slice is every n-th segment of 2048
+// reuse what is known about the row before.  A slice is every n-th segment of 1024
 // ids, since the ids that a history touches lie close together (common tokens have
 // low ids): with slices of neighbouring ids the blocks of the first slice took
 // 1.8 times as long as the others.  The block's warps have three jobs.  The
@@ -40,7 +40,8 @@ constexpr int kFirstProducer = kSumWarps + kPatchWarps;
 // a parity cannot tell from the phase before.)
 template <int RING>
 constexpr int rule_threads() { return (kFirstProducer + RING) * 32; }
-constexpr int kListCap = 512;                        // touched ids of a warp kept as a list
+constexpr int kHeld = 3;                             // of them in each lane's registers
+constexpr int kListCap = 256;                        // touched ids of a warp kept as a list
 constexpr uint32_t kCountFull = 0xffffu;             // a count that no longer fits
 constexpr int64_t kNoSeq = INT64_MIN;
 constexpr int kMaxNew = 6;                           // new tokens of a row handed on one by one
@@ -53,12 +54,12 @@ constexpr int kMaskCache = 256;                      // masks whose size is reme
 struct __align__(16) RowDesc {
     int32_t tok;                // the scored token's local number, or -1
     int32_t bad;                // status bits so far
-    int32_t flags;              // kDesc*
-    int32_t n_new;
+    int32_t flags;              // kDesc*, and from bit 8 on the number of new tokens
+    int32_t len;                // tokens of history
     int32_t fresh[kMaxNew];     // new tokens' local numbers, -1 or kFreshBad; kMade set: generated
     int32_t pad[2];
 };
-constexpr int32_t kDescRebuild = 1, kDescMask = 2, kDescSparse = 4;
+constexpr int32_t kDescRebuild = 1, kDescMask = 2, kDescSparse = 4, kDescNew = 256;
 // Narrow masks: copied by vectors while they would take at most this part of the
 // slice.  (A copy of 16 bytes takes a memory sector of its own, and time to issue;
 // bulk copies of 16 bytes would take more, as a warp issues them one by one.)
@@ -256,6 +257,8 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
                     else fresh = map.local(id);
                     if (fresh >= 0 && fresh != kFreshBad && n0 + lane >= w.prompt) fresh |= kMade;
                 }
+                // tokens of other slices are no news
+                if (!__any_sync(0xffffffffu, fresh != -1)) n_new = 0;
             }
         } else {
             w = row_rules(p, r);
@@ -356,7 +359,7 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
         RowDesc &d = sm.desc[s];
         if (lane < n_new) d.fresh[lane] = fresh;
         if (lane == 0) {
-            *reinterpret_cast<int4 *>(&d) = make_int4(tok_d, bad, flags, n_new);
+            *reinterpret_cast<int4 *>(&d) = make_int4(tok_d, bad, flags | n_new * kDescNew, n);
             if (flags & kDescRebuild) sm.rules[s] = w;
         }
         // each lane's own copies (if any), then what the warp has written
@@ -392,9 +395,10 @@ struct RuleWalk {
     uint32_t rebuilds = 0;
     RowRules w{};
     float inv_rho = 1.f;
-    // by lane: entry `lane` of the list, -1 if there is none
-    int32_t e_id = -1;
-    float e_pos = 1.f, e_neg = 1.f, e_add = 0.f;
+    // by lane: entries lane, lane + 32, ... of the list (local number, kMade set:
+    // seen; -1 if there is none) and what is added to their logits
+    int32_t e_id[kHeld];
+    float e_add[kHeld];
 
     __device__ RuleWalk(Smem &sm_, const RulesParams &p_, const SliceMap &map_)
         : sm(sm_), p(p_), lane(threadIdx.x & 31), wid((threadIdx.x >> 5) - kSumWarps), map(map_) {}
@@ -427,14 +431,16 @@ struct RuleWalk {
         return bias - (w.freq * (float)n + (n ? w.pres : 0.f));
     }
 
-    __device__ __forceinline__ void load_entry() {
-        e_id = -1;
-        if (n_list <= kListCap && lane < n_list) {
-            e_id = sm.list[wid][lane];
-            const bool seen = is_seen(e_id);
-            e_pos = seen ? inv_rho : 1.f;
-            e_neg = seen ? w.rho : 1.f;
-            e_add = summand(e_id, lane < n_bias ? sm.list_bias[wid][lane] : 0.f);
+    __device__ __forceinline__ void load_entries() {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            const int i = lane + 32 * j;
+            e_id[j] = -1;
+            if (n_list <= kListCap && i < n_list) {
+                const uint32_t d = sm.list[wid][i];
+                e_id[j] = (int32_t)d | (is_seen(d) ? kMade : 0);
+                e_add[j] = summand(d, i < n_bias ? sm.list_bias[wid][i] : 0.f);
+            }
         }
     }
 
@@ -532,7 +538,7 @@ struct RuleWalk {
             n_list += total;
         }
         __syncwarp();
-        load_entry();
+        load_entries();
         return true;
     }
 
@@ -551,12 +557,12 @@ struct RuleWalk {
     }
 
     // Moves to the row of the stage.  False on a timeout.
-    __device__ __forceinline__ bool enter_row(int s, int32_t flags, int32_t n_new) {
+    __device__ __forceinline__ bool enter_row(int s, int32_t flags, int32_t n) {
         if (flags & kDescRebuild) return rebuild(sm.rules[s]);
+        len = n;
         bool own = false;
-        for (int j = 0; j < n_new; ++j) {
+        for (int j = 0; j < flags / kDescNew; ++j) {
             const int32_t x = sm.desc[s].fresh[j];
-            ++len;
             if (x == kFreshBad) bad |= PS_DEV_BAD_TOKEN;
             if (x < 0 || x == kFreshBad) continue;
             const uint32_t id = (uint32_t)(x & ~kMade);
@@ -564,32 +570,39 @@ struct RuleWalk {
             insert(id, (x & kMade) != 0);
             own = true;
         }
-        if (own) load_entry();
+        if (own) load_entries();
         return true;
     }
 
-    // Calls f(d, factor of a positive logit, of another one, summand) for the lane's
-    // share of the warp's touched ids: each of them once in the warp.
+    // Calls f(j, d, factor of a positive logit, of another one, summand) for the lane's
+    // share of the warp's touched ids, each of them once in the warp: its j-th.
     template <typename F>
     __device__ __forceinline__ void for_touched(F f) const {
         if (n_list <= kListCap) {
-            if (e_id >= 0) f((uint32_t)e_id, e_pos, e_neg, e_add);
-            for (int i = lane + 32; i < n_list; i += 32) {
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j) {
+                if (n_list <= 32 * j) return;
+                const bool seen = e_id[j] & kMade;
+                if (e_id[j] >= 0)
+                    f(j, (uint32_t)(e_id[j] & ~kMade), seen ? inv_rho : 1.f, seen ? w.rho : 1.f, e_add[j]);
+            }
+            for (int i = lane + 32 * kHeld; i < n_list; i += 32) {
                 const uint32_t d = sm.list[wid][i];
                 const bool seen = is_seen(d);
-                f(d, seen ? inv_rho : 1.f, seen ? w.rho : 1.f,
+                f(i / 32, d, seen ? inv_rho : 1.f, seen ? w.rho : 1.f,
                   summand(d, i < n_bias ? sm.list_bias[wid][i] : 0.f));
             }
         } else {
+            int j = 0;
             for (int b = lane * kPatchWarps + wid; b * kBlockIds < map.nid; b += kPatchThreads) {
                 const uint32_t sw = sm.seen[b], bw = sm.biased[b];
                 for (uint32_t m = sw | bw; m != 0; m &= m - 1) {
-                    const int j = __ffs(m) - 1;
-                    const uint32_t d = b * kBlockIds + j;
-                    const bool seen = (sw >> j) & 1u;
-                    const float bias = (bw >> j) & 1u ? bias_of(w.bias_ids, w.bias_values, w.n_bias,
+                    const int k = __ffs(m) - 1;
+                    const uint32_t d = b * kBlockIds + k;
+                    const bool seen = (sw >> k) & 1u;
+                    const float bias = (bw >> k) & 1u ? bias_of(w.bias_ids, w.bias_values, w.n_bias,
                                                                 map.global((int32_t)d)) : 0.f;
-                    f(d, seen ? inv_rho : 1.f, seen ? w.rho : 1.f, summand(d, bias));
+                    f(j++, d, seen ? inv_rho : 1.f, seen ? w.rho : 1.f, summand(d, bias));
                 }
             }
         }

@@ -24,7 +24,7 @@ struct ProcessParams {
 
 // How the vocabulary is cut for the kernels that stream rows: into segments of
 // kSegIds ids, dealt to the slices in turn.
-constexpr int32_t kSegIds = 2048;
+constexpr int32_t kSegIds = 1024;
 struct RuleCut {
     int32_t n_segs;
     int32_t n_slices;

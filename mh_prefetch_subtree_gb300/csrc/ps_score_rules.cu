@@ -4,11 +4,12 @@
 // The formulation is ps_score_rows.cu's: sums relative to a reference, the token
 // left out.  ps_rule_rows.cuh brings the rows to the block.  Its patchers take the
 // token and the ids that penalties or biases touch out of the stage (their places
-// become -inf) and sum their processed float32 values on their own, so nothing is
-// rounded to the rows' type.  Each of the other 12 warps reads its ids into
-// registers, gives the stage back, applies the mask and sums: lane l of warp w has
-// blocks of 32 ids 12 (32 h + l) + (w + l) % 12, where the skew puts the lanes'
-// vectors in different banks.  What is left are 16 partial sums for each slice of a
+// become -inf) and hand their processed float32 values on apart, so nothing is
+// rounded to the rows' type.  (Summed by the patchers themselves, those values cost
+// the blocks with the most touched ids 30%.)  Each of the other 12 warps sums 64
+// (float32: 32) ids and one such value a lane, with the mask applied: lane l of warp
+// w has blocks of 32 ids 12 (32 h + l) + (w + l) % 12, where the skew puts the
+// lanes' vectors in different banks.  What is left are 16 partial sums for each slice of a
 // row, which a second kernel joins in their order.
 //
 // Where a mask leaves a lane at most kFewIds of its 64 (32 for float32) ids, the
@@ -26,13 +27,21 @@ namespace {
 
 constexpr int kRing = 3;
 constexpr int kFewIds = 10;
+static_assert(kHeld == kSumWarps / kPatchWarps, "what a patcher holds fits the summing lanes");
+constexpr int kTouched = kHeld * 32;   // one for each lane of the summing warps
 constexpr float kLeast = 8.673617379884035e-19f;     // 2^-60
 
 template <int DT>
 struct ScoreSmem : RuleSmem<DT, DT == PS_BF16 ? 2 : 1, kRing> {
     uint4 lut[DT == PS_BF16 ? 256 : 16];             // mask bits -> which words stay
     uint4 off[8];                                    // a block that does not count
+    // processed logits of the first touched ids of each patcher, and how many
+    float touched[kRing][kPatchWarps][kTouched];
+    int32_t n_touched[kRing][kPatchWarps];
 };
+
+static_assert(sizeof(ScoreSmem<PS_BF16>) <= 232448 && sizeof(ScoreSmem<PS_F32>) <= 232448,
+              "the shared memory of a block");
 
 __device__ __forceinline__ float warp_max_nan(float m) {
     float d;
@@ -75,7 +84,7 @@ __device__ __forceinline__ void add_term(Sums &a, float y, float g) {
 }
 
 template <int DT>
-__device__ __forceinline__ void pairs_of(uint4 q, float2 (&v)[DT == PS_BF16 ? 4 : 2]) {
+__device__ __forceinline__ void pairs_of(uint4 q, float2 *v) {
     if constexpr (DT == PS_BF16) {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -87,22 +96,101 @@ __device__ __forceinline__ void pairs_of(uint4 q, float2 (&v)[DT == PS_BF16 ? 4 
     }
 }
 
-// The sums of eight vectors.
-template <int DT, int NP, bool ENT>
-__device__ __forceinline__ Sums sum_dense(const uint4 (&q)[8], float ref, float g) {
+// A lane's ids in a stage: two runs of four vectors (for bfloat16 its two blocks,
+// for float32 the halves of its block), read in an order that spreads the lanes
+// over the banks, and the bits of the ids that count, in the same order.
+struct LaneIds {
+    const uint4 *a, *b;
+    int first;                  // vector to begin with
+    uint32_t ma, mb;            // its bits at the bottom
+};
+
+template <int DT>
+__device__ __forceinline__ uint4 masked_by(uint4 q, const uint4 *lut, uint32_t bits, uint32_t off) {
+    const uint4 k = lut[bits & (DT == PS_BF16 ? 0xffu : 15u)];
+    q.x = (q.x & k.x) | (off & ~k.x);
+    q.y = (q.y & k.y) | (off & ~k.y);
+    q.z = (q.z & k.z) | (off & ~k.z);
+    q.w = (q.w & k.w) | (off & ~k.w);
+    return q;
+}
+
+// Calls f(vector, vector) for the lane's pairs of vectors, those of b after those
+// of a.  A rolled loop: the eight vectors in one run of code would not fit the
+// instruction caches that three kinds of warps share.
+template <int DT, bool MASKED, typename F>
+__device__ __forceinline__ void each_pair(const LaneIds &l, const uint4 *lut, uint32_t off, F f) {
+    constexpr int kBits = DT == PS_BF16 ? 8 : 4;
+    int k = l.first;
+    uint4 qa = l.a[k], qb = l.b[k];
+    uint32_t ma = l.ma, mb = l.mb;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        k = (k + 1) & 3;
+        const uint4 na = l.a[k], nb = l.b[k];            // the next ones
+        if constexpr (MASKED) {
+            qa = masked_by<DT>(qa, lut, ma, off);
+            qb = masked_by<DT>(qb, lut, mb, off);
+            ma >>= kBits;
+            mb >>= kBits;
+        }
+        f(qa, qb);
+        qa = na;
+        qb = nb;
+    }
+}
+
+template <int DT, bool MASKED>
+__device__ __forceinline__ float max_of(const LaneIds &l, const uint4 *lut, uint32_t off) {
+    if constexpr (DT == PS_BF16) {
+        uint32_t m = 0xff80ff80u;
+        each_pair<DT, MASKED>(l, lut, off, [&](uint4 a, uint4 b) {
+            a.x = max_nan_bf16x2(max_nan_bf16x2(a.x, a.y), max_nan_bf16x2(a.z, a.w));
+            b.x = max_nan_bf16x2(max_nan_bf16x2(b.x, b.y), max_nan_bf16x2(b.z, b.w));
+            m = max_nan_bf16x2(m, max_nan_bf16x2(a.x, b.x));
+        });
+        return max_nan_f32(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    } else {
+        float m = -INFINITY;
+        each_pair<DT, MASKED>(l, lut, off, [&](uint4 a, uint4 b) {
+            const auto top = [](uint4 q) {
+                return max_nan_f32(max_nan_f32(__uint_as_float(q.x), __uint_as_float(q.y)),
+                                   max_nan_f32(__uint_as_float(q.z), __uint_as_float(q.w)));
+            };
+            m = max_nan_f32(m, max_nan_f32(top(a), top(b)));
+        });
+        return m;
+    }
+}
+
+// Raises -inf to the floor, which keeps 2^y y finite.
+template <int DT>
+__device__ __forceinline__ uint32_t raised(uint32_t w) {
+    if constexpr (DT == PS_BF16) return max_nan_bf16x2(w, kFloorBf16x2);
+    else return __float_as_uint(max_nan_f32(__uint_as_float(w), kFloorF32));
+}
+
+// The lane's sums.
+template <int DT, int NP, bool ENT, bool MASKED>
+__device__ __forceinline__ Sums sum_dense(const LaneIds &l, const uint4 *lut, uint32_t off, float ref,
+                                          float g, bool raise) {
     constexpr int kPairs = DT == PS_BF16 ? 4 : 2;
     const float2 L2 = make_float2(kLog2e, kLog2e), nR2 = make_float2(-ref, -ref);
     const float2 GL2 = make_float2(g * kLog2e, g * kLog2e), nGR2 = make_float2(-g * ref, -g * ref);
     float2 a1[4], at[4], ay[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) a1[j] = at[j] = ay[j] = make_float2(0.f, 0.f);
+    each_pair<DT, MASKED>(l, lut, off, [&](uint4 qa, uint4 qb) {
+        if (ENT && raise) {
+            qa = make_uint4(raised<DT>(qa.x), raised<DT>(qa.y), raised<DT>(qa.z), raised<DT>(qa.w));
+            qb = make_uint4(raised<DT>(qb.x), raised<DT>(qb.y), raised<DT>(qb.z), raised<DT>(qb.w));
+        }
+        float2 v[2 * kPairs];
+        pairs_of<DT>(qa, v);
+        pairs_of<DT>(qb, v + kPairs);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float2 v[kPairs];
-        pairs_of<DT>(q[i], v);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-            const int c = kPairs == 4 ? j : (i & 1) * 2 + j;
+        for (int j = 0; j < 2 * kPairs; ++j) {
+            const int c = j & 3;
             const float2 x = __ffma2_rn(v[j], L2, nR2);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             a1[c] = __fadd2_rn(a1[c], e);
@@ -117,46 +205,12 @@ __device__ __forceinline__ Sums sum_dense(const uint4 (&q)[8], float ref, float 
                 at[c] = __ffma2_rn(f, f, at[c]);
             }
         }
-    }
+    });
     Sums s;
     s.s1 = hsum4(a1);
     s.st = NP == 1 ? s.s1 : hsum4(at);
     s.y1 = ENT ? hsum4(ay) : 0.f;
     return s;
-}
-
-template <int DT>
-__device__ __forceinline__ float max_of(const uint4 (&q)[8]) {
-    if constexpr (DT == PS_BF16) {
-        uint32_t m = 0xff80ff80u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = max_nan_bf16x2(max_nan_bf16x2(max_nan_bf16x2(m, q[i].x), max_nan_bf16x2(q[i].y, q[i].z)),
-                               q[i].w);
-        return max_nan_f32(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-    } else {
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = max_nan_f32(max_nan_f32(max_nan_f32(m, __uint_as_float(q[i].x)),
-                                        max_nan_f32(__uint_as_float(q[i].y), __uint_as_float(q[i].z))),
-                            __uint_as_float(q[i].w));
-        return m;
-    }
-}
-
-// Raises -inf to the floor, which keeps 2^y y finite.
-template <int DT>
-__device__ __forceinline__ void raise_floor(uint4 (&q)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t *w = reinterpret_cast<uint32_t *>(&q[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == PS_BF16) w[j] = max_nan_bf16x2(w[j], kFloorBf16x2);
-            else w[j] = __float_as_uint(max_nan_f32(__uint_as_float(w[j]), kFloorF32));
-        }
-    }
 }
 
 // The patchers' rows: takes the token and the touched ids out of each stage and
@@ -169,6 +223,7 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
     const RuleSpan span(p.r.n_rows, p.cut.n_slices);
     int64_t r = span.t0 % span.rows;
     RuleWalk<Smem> walk(sm, p.r, SliceMap(p.cut, p.r.V, (int32_t)(span.t0 / span.rows)));
+    ChunkPart *at = p.parts + (r * p.cut.n_slices + walk.map.slice) * kScoreParts + kSumWarps + walk.wid;
     int s = 0;
     uint32_t lap = 0;
     for (int64_t t = span.t0; t < span.t1; ++t) {
@@ -177,8 +232,8 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
             return;
         }
         uint8_t *buf = sm.stage[s];
-        const int4 dh = *reinterpret_cast<const int4 *>(&sm.desc[s]);       // tok, bad, flags, n_new
-        if (((dh.z & kDescRebuild) || dh.w) && !walk.enter_row(s, dh.z, dh.w)) {
+        const int4 dh = *reinterpret_cast<const int4 *>(&sm.desc[s]);       // tok, bad, flags, len
+        if ((dh.z & ~(kDescMask | kDescSparse)) && !walk.enter_row(s, dh.z, dh.w)) {
             if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
             return;
         }
@@ -189,23 +244,27 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
             if (bad) set_status(p.r.status, bad);
             p.row_bad[r] = bad;
         }
-        float px = -INFINITY;                         // a touched id of this lane, and
-        Acc more = acc_empty();                       // its others
+        Acc more = acc_empty();                       // ids that find no place in `touched`
         auto put_off = [&](uint32_t d) {
             if constexpr (DT == PS_BF16) reinterpret_cast<uint16_t *>(buf)[d] = (uint16_t)kOff;
             else reinterpret_cast<uint32_t *>(buf)[d] = kOff;
         };
         auto allowed = [&](uint32_t d) { return mw == nullptr || ((mw[d >> 5] >> (d & 31)) & 1u); };
         if (!bad) {
-            walk.for_touched([&](uint32_t d, float pos, float neg, float add) {
+            if (walk.n_list > kListCap)               // then a lane's share may be less than its places
+#pragma unroll
+                for (int j = 0; j < kHeld; ++j) sm.touched[s][walk.wid][j * 32 + lane] = -INFINITY;
+            walk.for_touched([&](int j, uint32_t d, float pos, float neg, float add) {
                 float l = load_elem<DT>(buf, d);
                 put_off(d);
                 l = fmaf(l, l > 0.f ? pos : neg, add);
                 if (!allowed(d)) l = -INFINITY;
                 if ((int32_t)d == tok) {
                     p.tok_logit[r] = l;
-                } else if (px == -INFINITY) {
-                    px = l;
+                    l = -INFINITY;
+                }
+                if (j < kHeld) {
+                    sm.touched[s][walk.wid][j * 32 + lane] = l;
                 } else if (l != -INFINITY) {
                     const float x = l * kLog2e;
                     if (!(x <= more.R)) more = rebase<NP, ENT>(more, x, g);       // keeps a NaN
@@ -215,8 +274,8 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
                     more.y1 = fmaf(e, y, more.y1);
                 }
             });
-            if (tok >= 0 && owner_of(tok) == (uint32_t)walk.wid &&
-                !walk.is_seen(tok) && !walk.is_biased(tok) && lane == 0) {
+            if (tok >= 0 && lane == 0 && owner_of(tok) == (uint32_t)walk.wid && !walk.is_seen(tok) &&
+                !walk.is_biased(tok)) {
                 p.tok_logit[r] = allowed(tok) ? load_elem<DT>(buf, tok) : -INFINITY;
                 put_off(tok);
             }
@@ -224,28 +283,21 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
         // ids past the vocabulary in the last block
         if ((walk.map.nid & 31) && walk.wid == 0 && lane >= (walk.map.nid & 31))
             put_off((uint32_t)(walk.map.nid & ~31) + lane);
+        const int32_t n_list = bad ? 0 : walk.n_list;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.patched[s]);
+        if (lane == 0) {
+            sm.n_touched[s][walk.wid] = n_list <= kListCap ? n_list : -1;
+            mbar_arrive(&sm.patched[s]);
+        }
 
         ChunkPart part{-INFINITY, 0.f, 0.f, 0.f};
-        float m = max_nan_f32(px, more.R == more.R ? more.R * kLn2f : px);
-        m = warp_max_nan(m);
-        if (m != -INFINITY) {
-            const float ref = m * kLog2e;
-            Sums a{0.f, 0.f, 0.f};
-            if (px != -INFINITY) add_term<NP, ENT>(a, px * kLog2e - ref, g);
-            if (more.R != -INFINITY) {
-                const float d = more.R - ref, f = ex2(d);
-                a.s1 = fmaf(more.s1, f, a.s1);
-                if constexpr (NP != 1) a.st = fmaf(more.st[0], tau_term<NP>(d, f, g), a.st);
-                if constexpr (ENT) a.y1 += f * fmaf(d, more.s1, more.y1);
-            }
-            part.R = ref;
-            part.s1 = warp_sum(a.s1);
-            part.st = NP == 1 ? part.s1 : warp_sum(a.st);
-            if constexpr (ENT) part.y1 = warp_sum(a.y1);
+        if (n_list > kTouched) {
+            more = warp_merge<NP, ENT>(more, g);
+            part = ChunkPart{more.R, more.s1, more.st[0], more.y1};
+            if constexpr (NP == 1) part.st = part.s1;
         }
-        if (lane == 0) p.parts[(r * p.cut.n_slices + walk.map.slice) * kScoreParts + kSumWarps + walk.wid] = part;
+        if (lane == 0) *at = part;
+        at += p.cut.n_slices * kScoreParts;
         if (++s == kRing) {
             s = 0;
             ++lap;
@@ -253,6 +305,7 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
         if (++r == span.rows) {
             r = 0;
             walk.map = SliceMap(p.cut, p.r.V, walk.map.slice + 1);
+            at = p.parts + walk.map.slice * kScoreParts + kSumWarps + walk.wid;
         }
     }
 }
@@ -328,8 +381,14 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
             }
             few = __reduce_max_sync(0xffffffffu, few);
         }
+        // a touched id's processed logit for this lane (n: -1 means all places are written)
+        float px = -INFINITY;
+        if ((uint32_t)(wid / kPatchWarps * 32 + lane) < (uint32_t)sm.n_touched[s][wid % kPatchWarps])
+            px = sm.touched[s][wid % kPatchWarps][wid / kPatchWarps * 32 + lane];
         Sums sum{0.f, 0.f, 0.f};
-        auto join_lanes = [&](const Sums &a) {
+        auto join_lanes = [&](Sums a) {
+            if (px != -INFINITY) add_term<NP, ENT>(a, fmaf(px, kLog2e, -ref), g);
+            if constexpr (NP == 1) a.st = a.s1;
             sum.s1 = warp_sum(a.s1);
             sum.st = NP == 1 ? sum.s1 : warp_sum(a.st);
             if constexpr (ENT) sum.y1 = warp_sum(a.y1);
@@ -345,12 +404,12 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
                     for (uint32_t x = m[h]; x != 0; x &= x - 1)
                         f(load_elem<DT>(buf, (first + h * 32 * kSumWarps) * kBlockIds + __ffs(x) - 1));
             };
-            for (bool look = ENT; few > 0;) {
+            for (bool look = ENT; few > 0 || __any_sync(0xffffffffu, px != -INFINITY);) {
                 if (look) {
                     float x = -INFINITY;
                     each([&](float l) { x = max_nan_f32(x, l); });
                     if (x <= kAbsentBelow) x = -INFINITY;
-                    x = warp_max_nan(x);
+                    x = warp_max_nan(max_nan_f32(x, px));
                     if (x == -INFINITY) {
                         sum = Sums{0.f, 0.f, 0.f};
                         break;
@@ -365,55 +424,45 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
                 if (look || in_range()) break;
                 look = true;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[s]);
         } else {
-            uint4 q[8];
-#pragma unroll
-            for (int h = 0; h < kNb; ++h) {
-                const uint4 *v = m[h] ? reinterpret_cast<const uint4 *>(buf) + (first + h * 32 * kSumWarps) * kBv
-                                      : sm.off;
-#pragma unroll
-                for (int i = 0; i < kBv; ++i)         // in an order that spreads over the banks
-                    q[h * kBv + i] = v[kBv == 4 ? ((i + (lane >> 1)) & 3) : ((i + lane) & 7)];
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[s]);     // the stage is free
-            if (masked) {
-#pragma unroll
-                for (int h = 0; h < kNb; ++h) {
-                    // bits of vector i of the lane's order at the bottom of x
-                    const uint32_t x = kBv == 4 ? __funnelshift_r(m[h], m[h], 8 * ((lane >> 1) & 3))
-                                                : __funnelshift_r(m[h], m[h], 4 * (lane & 7));
-#pragma unroll
-                    for (int i = 0; i < kBv; ++i) {
-                        const uint4 k = sm.lut[kBv == 4 ? (x >> (8 * i)) & 0xffu : (x >> (4 * i)) & 15u];
-                        uint4 &v = q[h * kBv + i];
-                        v.x = (v.x & k.x) | (kOff & ~k.x);
-                        v.y = (v.y & k.y) | (kOff & ~k.y);
-                        v.z = (v.z & k.z) | (kOff & ~k.z);
-                        v.w = (v.w & k.w) | (kOff & ~k.w);
-                    }
-                }
+            LaneIds l;
+            const uint4 *v = reinterpret_cast<const uint4 *>(buf);
+            l.first = (kNb == 2 ? lane >> 1 : lane) & 3;
+            l.a = m[0] ? v + first * kBv : sm.off;
+            if constexpr (kNb == 2) {
+                l.b = m[1] ? v + (first + 32 * kSumWarps) * kBv : sm.off;
+                l.ma = __funnelshift_r(m[0], m[0], 8 * l.first);
+                l.mb = __funnelshift_r(m[1], m[1], 8 * l.first);
+            } else {
+                // a: the half of the block that puts the eight lanes of a bank sweep apart
+                const int half = (lane >> 2) & 1;
+                l.b = l.a + 4 * (half ^ 1);
+                l.a += 4 * half;
+                const uint32_t lo = m[0] & 0xffffu, hi = m[0] >> 16;
+                const uint32_t x = half ? hi : lo, y = half ? lo : hi;
+                l.ma = (x * 0x10001u) >> (4 * l.first);
+                l.mb = (y * 0x10001u) >> (4 * l.first);
             }
             // 0: with the reference at hand; 1: with the maximum; 2: with the maximum,
             // and -inf raised (among the logits it makes 2^y y NaN)
             for (int look = ENT;; ++look) {
-                if (look == 2) raise_floor<DT>(q);
-                if (look) {
-                    float x = max_of<DT>(q);
+                if (look == 1) {
+                    float x = masked ? max_of<DT, true>(l, sm.lut, kOff) : max_of<DT, false>(l, sm.lut, kOff);
                     if (x <= kAbsentBelow) x = -INFINITY;
-                    x = warp_max_nan(x);
+                    x = warp_max_nan(max_nan_f32(x, px));
                     if (x == -INFINITY) {             // nothing here
                         sum = Sums{0.f, 0.f, 0.f};
                         break;
                     }
                     ref = x * kLog2e;
                 }
-                join_lanes(sum_dense<DT, NP, ENT>(q, ref, g));
+                join_lanes(masked ? sum_dense<DT, NP, ENT, true>(l, sm.lut, kOff, ref, g, look == 2)
+                                  : sum_dense<DT, NP, ENT, false>(l, sm.lut, kOff, ref, g, look == 2));
                 if (ENT ? look == 2 || sum.y1 == sum.y1 || sum.s1 != sum.s1 : look || in_range()) break;
             }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[s]);
         if (lane == 0) *part = ChunkPart{sum.s1 == 0.f ? -INFINITY : ref, sum.s1, sum.st, sum.y1};
         part += p.cut.n_slices * kScoreParts;
         if (++s == kRing) {
