@@ -1,18 +1,24 @@
 // Logits rows from hidden states and a 4-bit output head (ps_head_rows).
 //
 // For few rows the weights are all that moves: V K / 2 bytes, each read once.
-// A warp takes 16 vocabulary rows and multiplies them by 8 hidden rows at a time
-// with m16n8k16 matrix instructions: the weights are the 16-row operand, made
-// in registers from the words that the lane has just loaded, so they never pass
+// A warp takes 16 MT vocabulary rows and multiplies them by 8 NT hidden rows with
+// m16n8k16 matrix instructions: the weights are the 16-row operand, made in
+// registers from the words that the lane has just loaded, so they never pass
 // through shared memory.  The order of k inside a product is free as long as
-// both operands have the same one, so it follows the packing: a lane loads
-// consecutive words of its row and takes elements j and j + 4 of a word as a
+// both operands have the same one, so it follows the packing: a lane loads 16
+// bytes of its row, 32 consecutive k, and takes elements j and j + 4 of a word as a
 // pair (one AND each).  The hidden rows are laid out once a block in shared
 // memory, in that order.
 //
 // 4-bit to bfloat16: 0x4300 | q is 128 + q exactly, and (128 + q) - (128 + zero)
 // is exact too, so the products have no rounding but the float32 sums'.  The
 // sums of a unit of k (a group, or 128 elements of one) are scaled in float32.
+// With groups of 32 or 64 a lane's 16 bytes are not spread over the four lanes
+// of a quad as one product needs them, so the quad first exchanges words.
+//
+// What bounds it: 8 weights take 11 instructions to unpack, 1 KB of weights about
+// 115 and another 16 for each 8 hidden rows, while a multiprocessor gets 1 KB
+// every 43 cycles from memory.
 #include <cuda_bf16.h>
 
 #include "ps_head.cuh"
@@ -20,9 +26,10 @@
 namespace ps {
 namespace {
 
-constexpr int kHeadThreads = 256;
-constexpr int kHeadWarps = kHeadThreads / 32;
-constexpr int kMaxStageK = 8192;      // hidden elements laid out at a time
+constexpr int kHeadWarps = 16;
+constexpr int kHeadThreads = kHeadWarps * 32;
+constexpr int kHeadSmem = 200 * 1024;  // for hidden rows
+constexpr int kMaxStageK = 8192;       // hidden elements laid out at a time, when not all fit
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -41,132 +48,357 @@ __device__ __forceinline__ uint32_t weight_pair(uint32_t word, int j, uint32_t z
     return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-__device__ __forceinline__ float load_scale(const HeadParams &p, int64_t i) {
-    if (p.head.scale_dtype == PS_BF16)
-        return __uint_as_float(
-            (uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p.head.scales) + i) << 16);
-    return __ldg(reinterpret_cast<const float *>(p.head.scales) + i);
+// The words of a quad's 128 k, 4 in each lane, regrouped so that each unit of U k
+// has U / 32 words in every lane: word slot `unit U/32 + i`.
+template <int U>
+__device__ __forceinline__ void spread(uint32_t (&q)[4], int tig) {
+    if constexpr (U == 128) return;
+    const bool hi = tig & 2;
+    const uint32_t r0 = __shfl_xor_sync(0xffffffffu, hi ? q[0] : q[2], 2);
+    const uint32_t r1 = __shfl_xor_sync(0xffffffffu, hi ? q[1] : q[3], 2);
+    // lanes 0, 1: their units' words 0, 1, then those of lanes 2, 3; lanes 2, 3:
+    // words 2, 3 of lanes 0, 1, then their own
+    uint32_t a0 = hi ? r0 : q[0], a1 = hi ? r1 : q[1], b0 = hi ? q[2] : r0, b1 = hi ? q[3] : r1;
+    if constexpr (U == 32) {
+        // (unit 0 or 1: a, unit 2 or 3: b) of the pair's lanes: one word of each to both
+        const bool odd = tig & 1;
+        const uint32_t ra = __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 1);
+        const uint32_t rb = __shfl_xor_sync(0xffffffffu, odd ? b0 : b1, 1);
+        const uint32_t ka = odd ? a1 : a0, kb = odd ? b1 : b0;
+        a0 = odd ? ra : ka;
+        a1 = odd ? ka : ra;
+        b0 = odd ? rb : kb;
+        b1 = odd ? kb : rb;
+    }
+    q[0] = a0;
+    q[1] = a1;
+    q[2] = b0;
+    q[3] = b1;
 }
 
-// U: elements of k whose sums share a scale (32, 64 or 128); a lane holds U / 32
-// words of each of its two rows.  wk warps of a block share a tile's k.
+// Where the 8 k from 8 c on are after spread(): the lane of the quad and the slot.
 template <int U>
-__global__ void __launch_bounds__(kHeadThreads) head_rows_kernel(const HeadParams p, int wk) {
+__device__ __forceinline__ void place(int c, int &tig, int &slot) {
+    const int lane = c / 4, w = c % 4;               // as loaded
+    if constexpr (U == 128) {
+        tig = lane;
+        slot = w;
+    } else if constexpr (U == 64) {
+        tig = (lane & 1) | (w & 2);
+        slot = (lane & 2) | (w & 1);
+    } else {
+        // word w of lane (its unit) goes to lane w
+        tig = w;
+        slot = lane;
+    }
+}
+
+template <int SD>
+__device__ __forceinline__ float load_scale(const void *scales, int64_t i) {
+    if constexpr (SD == PS_BF16)
+        return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(scales) + i) << 16);
+    else
+        return __ldg(reinterpret_cast<const float *>(scales) + i);
+}
+
+// U: elements of k whose sums share a scale (32, 64 or 128).  wk warps of a block
+// share a tile's k.  K is laid out whole, or where it does not fit (then NT is 1)
+// in parts that all warps of the block work on together.
+template <int U, int NT, int MT, int SD>
+__global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadParams p, int wk, int stage_k) {
     extern __shared__ __align__(16) uint4 smem4[];
-    constexpr int W = U / 32;
-    __shared__ float part[kHeadWarps][16][8];
+    constexpr int W = U / 32;                        // words of a unit in a lane
+    constexpr int kPf = NT == 1 ? (U == 32 ? 3 : 4) : (NT == 2 ? 3 : 2);    // 128-k steps in flight
+    constexpr int kRows = 16 * MT, kCols = 8 * NT;
+    float *part = reinterpret_cast<float *>(smem4 + (size_t)NT * stage_k);      // [warps][kCols][kRows]
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int g = lane >> 2, tig = lane & 3;
-    const int32_t V = p.head.V, K = p.head.K;
-    const int64_t groups = K / p.head.group;
-    const int n0 = blockIdx.y * 8;
-    const int64_t n_tiles = ((int64_t)V + 15) / 16;
+    const int32_t V = p.head.V, K = p.head.K, group = p.head.group;
+    const int64_t groups = K / group;
+    const int64_t n_tiles = ((int64_t)V + kRows - 1) / kRows;
     const int per = kHeadWarps / wk, kw = wid % wk;
-    const bool one = K <= kMaxStageK;
-    for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < n_tiles; t0 += (int64_t)gridDim.x * per) {
-        const int64_t tile = t0 + wid / wk;
-        const int64_t r0 = min(tile * 16 + g, (int64_t)V - 1), r1 = min(tile * 16 + g + 8, (int64_t)V - 1);
-        float total[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int32_t ks = 0; ks < K; ks += kMaxStageK) {
-            const int32_t kn = min(kMaxStageK, K - ks);
-            if (!one || t0 == (int64_t)blockIdx.x * per) {
+    const int n_cols = (p.n_rows + kCols - 1) / kCols;
+    const int64_t n_work = (n_tiles + per - 1) / per * n_cols;
+    int laid_n0 = -1;
+    for (int64_t work = blockIdx.x; work < n_work; work += gridDim.x) {
+        // blocks next to each other take the same weights for other rows
+        const int n0 = (int)(work % n_cols) * kCols;
+        const int64_t t0 = work / n_cols * per, tile = t0 + wid / wk;
+        const bool live = tile < n_tiles;
+        int64_t row[MT][2];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            row[i][0] = min(tile * kRows + i * 16 + g, (int64_t)V - 1);
+            row[i][1] = min(tile * kRows + i * 16 + g + 8, (int64_t)V - 1);
+        }
+        float total[MT][NT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) total[i][n][j] = 0.f;
+        for (int32_t ks = 0; ks < K; ks += stage_k) {
+            const int32_t kn = min(stage_k, K - ks);
+            if (stage_k < K || laid_n0 != n0) {
+                laid_n0 = n0;
                 __syncthreads();
-                for (int i = threadIdx.x; i < kn; i += kHeadThreads) {     // kn / 8 * 8 rows
-                    const int n = i & 7, c = i >> 3;                        // 8 elements from k = 8 c
-                    const int u = c / (U / 8), in = c % (U / 8);
-                    const int tg = in / W, w = in % W;
+                for (int i = threadIdx.x; i < NT * kn; i += kHeadThreads) {
+                    const int n = i % kCols, c = i / kCols;             // 8 k from ks + 8 c on
                     uint4 h = make_uint4(0, 0, 0, 0);
                     if (n0 + n < p.n_rows)
                         h = __ldg(reinterpret_cast<const uint4 *>(
                             p.hidden + (int64_t)(n0 + n) * p.hidden_ld + ks + c * 8));
+                    int tg, at;
+                    if (c / 16 < kn / 128) {
+                        place<U>(c % 16, tg, at);
+                        at += c / 16 * 4;
+                    } else {                                            // the rest: units one by one
+                        const int u = c / (U / 8), in = c % (U / 8);
+                        tg = in / W;
+                        at = u * W + in % W;
+                    }
                     // pairs (0, 4), (1, 5), (2, 6), (3, 7)
-                    uint4 o;
-                    o.x = __byte_perm(h.x, h.z, 0x5410);
-                    o.y = __byte_perm(h.x, h.z, 0x7632);
-                    o.z = __byte_perm(h.y, h.w, 0x5410);
-                    o.w = __byte_perm(h.y, h.w, 0x7632);
-                    smem4[(u * W + w) * 32 + n * 4 + tg] = o;
+                    smem4[(size_t)(n / 8) * kn + at * 32 + (n % 8) * 4 + tg] =
+                        make_uint4(__byte_perm(h.x, h.z, 0x5410), __byte_perm(h.x, h.z, 0x7632),
+                                   __byte_perm(h.y, h.w, 0x5410), __byte_perm(h.y, h.w, 0x7632));
                 }
                 __syncthreads();
             }
-            if (tile < n_tiles) {
-                const uint8_t *q0 = p.head.q + r0 * (K / 2) + ks / 2 + tig * (U / 8);
-                const uint8_t *q1 = p.head.q + r1 * (K / 2) + ks / 2 + tig * (U / 8);
-                for (int u = kw; u < kn / U; u += wk) {
-                    uint32_t a[W], b[W];
+            if (!live) continue;
+            // the sums of one unit from the lane's words of it
+            auto unit = [&](const uint32_t *(&a)[MT], const uint32_t *(&b)[MT], int at, const float (&s)[MT][2],
+                            const uint32_t (&z)[MT][2]) {
+                float c[MT][NT][4];
 #pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        a[w] = __ldg(reinterpret_cast<const uint32_t *>(q0 + (int64_t)u * (U / 2)) + w);
-                        b[w] = __ldg(reinterpret_cast<const uint32_t *>(q1 + (int64_t)u * (U / 2)) + w);
-                    }
-                    const int64_t gr = (ks + u * U) / p.head.group;
-                    const float s0 = load_scale(p, r0 * groups + gr), s1 = load_scale(p, r1 * groups + gr);
-                    uint32_t z0 = 8, z1 = 8;
-                    if (p.head.zeros) {
-                        z0 = __ldg(p.head.zeros + r0 * groups + gr) & 15u;
-                        z1 = __ldg(p.head.zeros + r1 * groups + gr) & 15u;
-                    }
-                    z0 = 0x43004300u | z0 * 0x10001u;
-                    z1 = 0x43004300u | z1 * 0x10001u;
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        const uint4 h = smem4[(u * W + w) * 32 + lane];
-                        mma16816(c, weight_pair(a[w], 0, z0), weight_pair(b[w], 0, z1),
-                                 weight_pair(a[w], 1, z0), weight_pair(b[w], 1, z1), h.x, h.y);
-                        mma16816(c, weight_pair(a[w], 2, z0), weight_pair(b[w], 2, z1),
-                                 weight_pair(a[w], 3, z0), weight_pair(b[w], 3, z1), h.z, h.w);
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) c[i][n][j] = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    uint4 h[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) h[n] = smem4[(size_t)n * kn + (at + w) * 32 + lane];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        uint32_t x[4], y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            x[j] = weight_pair(a[i][w], j, z[i][0]);
+                            y[j] = weight_pair(b[i][w], j, z[i][1]);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma16816(c[i][n], x[0], y[0], x[1], y[1], h[n].x, h[n].y);
+                            mma16816(c[i][n], x[2], y[2], x[3], y[3], h[n].z, h[n].w);
+                        }
                     }
-                    total[0] = fmaf(s0, c[0], total[0]);
-                    total[1] = fmaf(s0, c[1], total[1]);
-                    total[2] = fmaf(s1, c[2], total[2]);
-                    total[3] = fmaf(s1, c[3], total[3]);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            total[i][n][j] = fmaf(s[i][j >> 1], c[i][n][j], total[i][n][j]);
+            };
+            auto scales_of = [&](int32_t k, float (&s)[MT][2], uint32_t (&z)[MT][2]) {
+                const int64_t gr = k / group;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        s[i][j] = load_scale<SD>(p.head.scales, row[i][j] * groups + gr);
+                        z[i][j] = p.head.zeros ? __ldg(p.head.zeros + row[i][j] * groups + gr) & 15u : 8u;
+                    }
+            };
+            const int n_step = kn / 128;
+            uint4 buf[kPf][MT][2];
+            float sc[4 / W][MT][2];                  // the next step's
+            uint32_t ze[4 / W][MT][2];
+            auto fetch_scales = [&](int st) {
+                if (st >= n_step) return;
+#pragma unroll
+                for (int u = 0; u < 4 / W; ++u) scales_of(ks + st * 128 + u * U, sc[u], ze[u]);
+            };
+            auto fetch = [&](int st, int f) {
+                if (st >= n_step) return;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        buf[f][i][j] = __ldcs(reinterpret_cast<const uint4 *>(
+                            p.head.q + row[i][j] * (K / 2) + ks / 2 + st * 64 + tig * 16));
+            };
+#pragma unroll
+            for (int f = 0; f < kPf; ++f) fetch(kw + f * wk, f);
+            fetch_scales(kw);
+            for (int st = kw; st < n_step; st += kPf * wk) {
+#pragma unroll
+                for (int f = 0; f < kPf; ++f) {
+                    const int now = st + f * wk;
+                    if (now < n_step) {
+                        uint32_t q[MT][2][4];
+                        float s[4 / W][MT][2];
+                        uint32_t z[4 / W][MT][2];
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                q[i][j][0] = buf[f][i][j].x;
+                                q[i][j][1] = buf[f][i][j].y;
+                                q[i][j][2] = buf[f][i][j].z;
+                                q[i][j][3] = buf[f][i][j].w;
+#pragma unroll
+                                for (int u = 0; u < 4 / W; ++u) {
+                                    s[u][i][j] = sc[u][i][j];
+                                    z[u][i][j] = 0x43004300u | ze[u][i][j] * 0x10001u;
+                                }
+                            }
+                        fetch(now + kPf * wk, f);
+                        fetch_scales(now + wk);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            spread<U>(q[i][0], tig);
+                            spread<U>(q[i][1], tig);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4 / W; ++u) {
+                            const uint32_t *a[MT], *b[MT];
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) {
+                                a[i] = &q[i][0][u * W];
+                                b[i] = &q[i][1][u * W];
+                            }
+                            unit(a, b, now * 4 + u * W, s[u], z[u]);
+                        }
+                    }
+                }
+            }
+            // what is left of k after whole steps: units, by the words of the unit
+            if constexpr (U < 128) {
+                for (int u = n_step * (4 / W) + kw; u < kn / U; u += wk) {
+                    uint32_t q[MT][2][W];
+                    const uint32_t *a[MT], *b[MT];
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int w = 0; w < W; ++w)
+                                q[i][j][w] = __ldg(reinterpret_cast<const uint32_t *>(
+                                    p.head.q + row[i][j] * (K / 2) + ks / 2 + (int64_t)u * (U / 2) +
+                                    tig * (U / 8)) + w);
+                        a[i] = q[i][0];
+                        b[i] = q[i][1];
+                    }
+                    float s[MT][2];
+                    uint32_t z[MT][2];
+                    scales_of(ks + u * U, s, z);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) z[i][j] = 0x43004300u | z[i][j] * 0x10001u;
+                    unit(a, b, u * W, s, z);
                 }
             }
         }
-        // join the warps of a tile in order, then store
-        __syncthreads();
-        part[wid][g][tig * 2] = total[0];
-        part[wid][g][tig * 2 + 1] = total[1];
-        part[wid][g + 8][tig * 2] = total[2];
-        part[wid][g + 8][tig * 2 + 1] = total[3];
-        __syncthreads();
-        for (int i = threadIdx.x; i < per * 128; i += kHeadThreads) {
-            const int t = i / 128, n = (i / 16) % 8, m = i % 16;
-            const int64_t v = (t0 + t) * 16 + m;
-            if (v >= V || n0 + n >= p.n_rows) continue;
-            float x = 0.f;
-            for (int j = 0; j < wk; ++j) x += part[t * wk + j][m][n];
+        auto store = [&](int n, int64_t v, float x) {
+            if (v >= V || n0 + n >= p.n_rows) return;
             const int64_t at = (int64_t)(n0 + n) * p.ld + v;
             if (p.dtype == PS_BF16)
                 reinterpret_cast<__nv_bfloat16 *>(p.logits)[at] = __float2bfloat16_rn(x);
             else
                 reinterpret_cast<float *>(p.logits)[at] = x;
+        };
+        if (wk == 1) {
+            if (live)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            store(n * 8 + tig * 2 + (j & 1), tile * kRows + i * 16 + g + (j >> 1) * 8,
+                                  total[i][n][j]);
+        } else {
+            // join the warps of a tile in order
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        part[(wid * kCols + n * 8 + tig * 2 + (j & 1)) * kRows + i * 16 + g + (j >> 1) * 8] =
+                            total[i][n][j];
+            __syncthreads();
+            for (int i = threadIdx.x; i < per * kCols * kRows; i += kHeadThreads) {
+                const int t = i / (kCols * kRows), n = i / kRows % kCols, m = i % kRows;
+                float x = 0.f;
+                for (int j = 0; j < wk; ++j) x += part[((t * wk + j) * kCols + n) * kRows + m];
+                store(n, (t0 + t) * kRows + m, x);
+            }
         }
     }
 }
 
-template <int U>
+// Warps that share a tile's k: as few as give every warp work, and of those the
+// number that leaves the least of it over in the last round.
+int split_k(int64_t tiles, int64_t cols, int sms, int steps) {
+    int best = 1;
+    double least = 1e30;
+    for (int wk = 1; wk <= kHeadWarps && (wk == 1 || wk <= steps); wk *= 2) {
+        const int64_t per = kHeadWarps / wk, work = (tiles + per - 1) / per * cols;
+        const double rounds = (double)((work + sms - 1) / sms) / wk;
+        if (rounds < 0.9 * least) {
+            least = rounds;
+            best = wk;
+        }
+    }
+    return best;
+}
+
+template <int U, int NT, int MT, int SD>
 cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
-    const int smem = (p.head.K < kMaxStageK ? p.head.K : kMaxStageK) * 16;
-    cudaError_t e = cudaFuncSetAttribute(head_rows_kernel<U>,
+    const int K = p.head.K;
+    const int stage_k = (int64_t)NT * K * 16 <= kHeadSmem ? K : kMaxStageK;
+    const int64_t tiles = ((int64_t)p.head.V + 16 * MT - 1) / (16 * MT);
+    const int64_t cols = ((int64_t)p.n_rows + 8 * NT - 1) / (8 * NT);
+    const int wk = split_k(tiles, cols, sms, K / (U < 128 ? U : 128));
+    const int smem = NT * stage_k * 16 + (wk > 1 ? kHeadWarps * 16 * MT * 8 * NT * 4 : 0);
+    cudaError_t e = cudaFuncSetAttribute(head_rows_kernel<U, NT, MT, SD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = ((int64_t)p.head.V + 15) / 16;
-    int wk = 1;
-    while (wk < kHeadWarps && tiles * wk < (int64_t)sms * 16) wk *= 2;
-    const int64_t per = kHeadWarps / wk, want = (tiles + per - 1) / per, most = (int64_t)sms * 2;
-    const dim3 grid((unsigned)(want < most ? want : most), (unsigned)((p.n_rows + 7) / 8));
-    head_rows_kernel<U><<<grid, kHeadThreads, smem, stream>>>(p, wk);
+    const int64_t per = kHeadWarps / wk, work = (tiles + per - 1) / per * cols;
+    head_rows_kernel<U, NT, MT, SD>
+        <<<(unsigned)(work < sms ? work : sms), kHeadThreads, smem, stream>>>(p, wk, stage_k);
     return cudaGetLastError();
+}
+
+// Hidden rows of a block: 8, 16 or 32, as many as there are and as fit.
+template <int U, int SD>
+cudaError_t launch_n(const HeadParams &p, int sms, cudaStream_t stream) {
+    const int64_t fits = kHeadSmem / ((int64_t)p.head.K * 16);
+    if (p.n_rows > 16 && fits >= 4) return launch<U, 4, 1, SD>(p, sms, stream);
+    if (p.n_rows > 8 && fits >= 2) return launch<U, 2, 1, SD>(p, sms, stream);
+    return launch<U, 1, 1, SD>(p, sms, stream);
+}
+
+template <int U>
+cudaError_t launch_u(const HeadParams &p, int sms, cudaStream_t stream) {
+    return p.head.scale_dtype == PS_BF16 ? launch_n<U, PS_BF16>(p, sms, stream)
+                                         : launch_n<U, PS_F32>(p, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_head_rows(const HeadParams &p, int sms, cudaStream_t stream) {
-    if (p.head.group == 32) return launch<32>(p, sms, stream);
-    if (p.head.group == 64) return launch<64>(p, sms, stream);
-    return launch<128>(p, sms, stream);
+    if (p.head.group == 32) return launch_u<32>(p, sms, stream);
+    if (p.head.group == 64) return launch_u<64>(p, sms, stream);
+    return launch_u<128>(p, sms, stream);
 }
 
 }  // namespace ps
