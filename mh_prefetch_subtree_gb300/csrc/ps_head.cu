@@ -93,18 +93,15 @@ __device__ __forceinline__ void place(int c, int &tig, int &slot) {
     }
 }
 
-template <int SD>
-__device__ __forceinline__ float load_scale(const void *scales, int64_t i) {
-    if constexpr (SD == PS_BF16)
-        return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(scales) + i) << 16);
-    else
-        return __ldg(reinterpret_cast<const float *>(scales) + i);
+__device__ __forceinline__ float load_scale(const uint16_t *p) {
+    return __uint_as_float((uint32_t)__ldg(p) << 16);
 }
+__device__ __forceinline__ float load_scale(const float *p) { return __ldg(p); }
 
 // U: elements of k whose sums share a scale (32, 64 or 128).  wk warps of a block
 // share a tile's k.  K is laid out whole, or where it does not fit (then NT is 1)
 // in parts that all warps of the block work on together.
-template <int U, int NT, int MT, int SD>
+template <int U, int NT, int MT, typename ScaleT>
 __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadParams p, int wk, int stage_k) {
     extern __shared__ __align__(16) uint4 smem4[];
     constexpr int W = U / 32;                        // words of a unit in a lane
@@ -113,8 +110,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
     float *part = reinterpret_cast<float *>(smem4 + (size_t)NT * stage_k);      // [warps][kCols][kRows]
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int g = lane >> 2, tig = lane & 3;
-    const int32_t V = p.head.V, K = p.head.K, group = p.head.group;
-    const int64_t groups = K / group;
+    const int32_t V = p.head.V, K = p.head.K;
+    const int64_t groups = K / p.head.group;
+    // a 128-k step's group, where groups are longer: step / (group / 128)
+    const uint32_t long_group = U == 128 && p.head.group > 128 ? 0xffffffffu / (p.head.group / 128) + 1 : 0;
     const int64_t n_tiles = ((int64_t)V + kRows - 1) / kRows;
     const int per = kHeadWarps / wk, kw = wid % wk;
     const int n_cols = (p.n_rows + kCols - 1) / kCols;
@@ -125,12 +124,17 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
         const int n0 = (int)(work % n_cols) * kCols;
         const int64_t t0 = work / n_cols * per, tile = t0 + wid / wk;
         const bool live = tile < n_tiles;
-        int64_t row[MT][2];
+        const uint8_t *wq[MT][2], *wz[MT][2];        // the lane's rows: weights, zeros,
+        const ScaleT *ws[MT][2];                     // scales
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            row[i][0] = min(tile * kRows + i * 16 + g, (int64_t)V - 1);
-            row[i][1] = min(tile * kRows + i * 16 + g + 8, (int64_t)V - 1);
-        }
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t row = min(tile * kRows + i * 16 + j * 8 + g, (int64_t)V - 1);
+                wq[i][j] = p.head.q + row * (K / 2) + tig * 16;
+                ws[i][j] = reinterpret_cast<const ScaleT *>(p.head.scales) + row * groups;
+                wz[i][j] = p.head.zeros + (p.head.zeros ? row * groups : 0);
+            }
         float total[MT][NT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -204,14 +208,15 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
                         for (int j = 0; j < 4; ++j)
                             total[i][n][j] = fmaf(s[i][j >> 1], c[i][n][j], total[i][n][j]);
             };
-            auto scales_of = [&](int32_t k, float (&s)[MT][2], uint32_t (&z)[MT][2]) {
-                const int64_t gr = k / group;
+            // of unit u, counted from k = 0
+            auto scales_of = [&](uint32_t u, float (&s)[MT][2], uint32_t (&z)[MT][2]) {
+                if (U == 128 && long_group) u = __umulhi(u, long_group);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        s[i][j] = load_scale<SD>(p.head.scales, row[i][j] * groups + gr);
-                        z[i][j] = p.head.zeros ? __ldg(p.head.zeros + row[i][j] * groups + gr) & 15u : 8u;
+                        s[i][j] = load_scale(ws[i][j] + u);
+                        z[i][j] = p.head.zeros ? __ldg(wz[i][j] + u) & 15u : 8u;
                     }
             };
             const int n_step = kn / 128;
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
             auto fetch_scales = [&](int st) {
                 if (st >= n_step) return;
 #pragma unroll
-                for (int u = 0; u < 4 / W; ++u) scales_of(ks + st * 128 + u * U, sc[u], ze[u]);
+                for (int u = 0; u < 4 / W; ++u) scales_of(ks / U + st * (4 / W) + u, sc[u], ze[u]);
             };
             auto fetch = [&](int st, int f) {
                 if (st >= n_step) return;
@@ -229,8 +234,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        buf[f][i][j] = __ldcs(reinterpret_cast<const uint4 *>(
-                            p.head.q + row[i][j] * (K / 2) + ks / 2 + st * 64 + tig * 16));
+                        buf[f][i][j] = __ldcs(reinterpret_cast<const uint4 *>(wq[i][j] + ks / 2) + st * 4);
             };
 #pragma unroll
             for (int f = 0; f < kPf; ++f) fetch(kw + f * wk, f);
@@ -289,14 +293,13 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
 #pragma unroll
                             for (int w = 0; w < W; ++w)
                                 q[i][j][w] = __ldg(reinterpret_cast<const uint32_t *>(
-                                    p.head.q + row[i][j] * (K / 2) + ks / 2 + (int64_t)u * (U / 2) +
-                                    tig * (U / 8)) + w);
+                                    wq[i][j] - tig * 16 + ks / 2 + u * (U / 2) + tig * (U / 8)) + w);
                         a[i] = q[i][0];
                         b[i] = q[i][1];
                     }
                     float s[MT][2];
                     uint32_t z[MT][2];
-                    scales_of(ks + u * U, s, z);
+                    scales_of(ks / U + u, s, z);
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -361,7 +364,7 @@ int split_k(int64_t tiles, int64_t cols, int sms, int steps) {
     return best;
 }
 
-template <int U, int NT, int MT, int SD>
+template <int U, int NT, int MT, typename ScaleT>
 cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     const int K = p.head.K;
     const int stage_k = (int64_t)NT * K * 16 <= kHeadSmem ? K : kMaxStageK;
@@ -369,28 +372,28 @@ cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     const int64_t cols = ((int64_t)p.n_rows + 8 * NT - 1) / (8 * NT);
     const int wk = split_k(tiles, cols, sms, K / (U < 128 ? U : 128));
     const int smem = NT * stage_k * 16 + (wk > 1 ? kHeadWarps * 16 * MT * 8 * NT * 4 : 0);
-    cudaError_t e = cudaFuncSetAttribute(head_rows_kernel<U, NT, MT, SD>,
+    cudaError_t e = cudaFuncSetAttribute(head_rows_kernel<U, NT, MT, ScaleT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t per = kHeadWarps / wk, work = (tiles + per - 1) / per * cols;
-    head_rows_kernel<U, NT, MT, SD>
+    head_rows_kernel<U, NT, MT, ScaleT>
         <<<(unsigned)(work < sms ? work : sms), kHeadThreads, smem, stream>>>(p, wk, stage_k);
     return cudaGetLastError();
 }
 
 // Hidden rows of a block: 8, 16 or 32, as many as there are and as fit.
-template <int U, int SD>
+template <int U, typename ScaleT>
 cudaError_t launch_n(const HeadParams &p, int sms, cudaStream_t stream) {
     const int64_t fits = kHeadSmem / ((int64_t)p.head.K * 16);
-    if (p.n_rows > 16 && fits >= 4) return launch<U, 4, 1, SD>(p, sms, stream);
-    if (p.n_rows > 8 && fits >= 2) return launch<U, 2, 1, SD>(p, sms, stream);
-    return launch<U, 1, 1, SD>(p, sms, stream);
+    if (p.n_rows > 16 && fits >= 4) return launch<U, 4, 1, ScaleT>(p, sms, stream);
+    if (p.n_rows > 8 && fits >= 2) return launch<U, 2, 1, ScaleT>(p, sms, stream);
+    return launch<U, 1, 1, ScaleT>(p, sms, stream);
 }
 
 template <int U>
 cudaError_t launch_u(const HeadParams &p, int sms, cudaStream_t stream) {
-    return p.head.scale_dtype == PS_BF16 ? launch_n<U, PS_BF16>(p, sms, stream)
-                                         : launch_n<U, PS_F32>(p, sms, stream);
+    return p.head.scale_dtype == PS_BF16 ? launch_n<U, uint16_t>(p, sms, stream)
+                                         : launch_n<U, float>(p, sms, stream);
 }
 
 }  // namespace
