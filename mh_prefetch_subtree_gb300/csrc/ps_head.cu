@@ -10,15 +10,23 @@
 // pair (one AND each).  The hidden rows are laid out once a block in shared
 // memory, in that order.
 //
-// 4-bit to bfloat16: 0x4300 | q is 128 + q exactly, and (128 + q) - (128 + zero)
-// is exact too, so the products have no rounding but the float32 sums'.  The
-// sums of a unit of k (a group, or 128 elements of one) are scaled in float32.
-// With groups of 32 or 64 a lane's 16 bytes are not spread over the four lanes
-// of a quad as one product needs them, so the quad first exchanges words.
+// 4-bit to float16: 0x6400 | q is 1024 + q and 0x6400 | 16 q is 1024 + 16 q, so two
+// of a word's pairs need no shift, and 1024 + q - (1024 + zero) and
+// (1024 + 16 q) / 16 - (64 + zero) are exact.  (In bfloat16, with 7 bits of
+// mantissa, every pair but one needs a shift: 1 row of 151936 x 4096 took 80 us,
+// bound by the integer pipe.)  The hidden rows become float16 as well: each is
+// scaled by the power of two that brings its largest element to 2^14 .. 2^15,
+// which is taken back at the end.  That is exact but for elements below 2^-29 of
+// the largest, which are rounded to a multiple of 2^-39 of it or so, far below the
+// float32 sums' own rounding.  The sums of a unit of k (a group, or 128 elements of
+// one) are scaled in float32.  With groups of 32 or 64 a lane's 16 bytes are not
+// spread over the four lanes of a quad as one product needs them, so the quad
+// first exchanges words.
 //
-// What bounds it: 8 weights take 11 instructions to unpack, 1 KB of weights about
-// 115 and another 16 for each 8 hidden rows, while a multiprocessor gets 1 KB
+// What bounds it: 8 weights take 9 instructions to unpack, 5 of them on the integer
+// pipe, which takes one every other cycle; a multiprocessor gets 1 KB of weights
 // every 43 cycles from memory.
+#include <cuda_fp16.h>
 #include <cuda_bf16.h>
 
 #include "ps_head.cuh"
@@ -34,18 +42,24 @@ constexpr int kMaxStageK = 8192;       // hidden elements laid out at a time, wh
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Elements j and j + 4 of a word, less the zero, as two bfloat16.
-__device__ __forceinline__ uint32_t weight_pair(uint32_t word, int j, uint32_t zero128) {
-    const uint32_t t = ((word >> (4 * j)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&t),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&zero128));
-    return *reinterpret_cast<const uint32_t *>(&d);
+__device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
+__device__ __forceinline__ __half2 h2_of(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
+
+// The four pairs (j, j + 4) of a word less the zero, as float16.  z1 holds
+// -(1024 + zero) twice, z16 -(64 + zero).
+__device__ __forceinline__ void unpack(uint32_t word, uint32_t z1, uint32_t z16, uint32_t (&x)[4]) {
+    const uint32_t w8 = word >> 8;
+    const __half2 sixteenth = h2_of(0x2c002c00u);
+    x[0] = h2_bits(__hadd2(h2_of((word & 0x000f000fu) | 0x64006400u), h2_of(z1)));
+    x[1] = h2_bits(__hfma2(h2_of((word & 0x00f000f0u) | 0x64006400u), sixteenth, h2_of(z16)));
+    x[2] = h2_bits(__hadd2(h2_of((w8 & 0x000f000fu) | 0x64006400u), h2_of(z1)));
+    x[3] = h2_bits(__hfma2(h2_of((w8 & 0x00f000f0u) | 0x64006400u), sixteenth, h2_of(z16)));
 }
 
 // The words of a quad's 128 k, 4 in each lane, regrouped so that each unit of U k
@@ -93,10 +107,41 @@ __device__ __forceinline__ void place(int c, int &tig, int &slot) {
     }
 }
 
-__device__ __forceinline__ float load_scale(const uint16_t *p) {
-    return __uint_as_float((uint32_t)__ldg(p) << 16);
+// A scale and its group's zero, as one or two words.
+template <typename ScaleT>
+struct ScaleZero;
+template <>
+struct ScaleZero<uint16_t> {
+    uint32_t w;
+    __device__ __forceinline__ void load(const uint16_t *s, const uint8_t *z) {
+        w = (uint32_t)__ldg(s) << 16 | (z ? __ldg(z) & 15u : 8u);
+    }
+    __device__ __forceinline__ ScaleZero from(int lane) const {
+        return ScaleZero{__shfl_sync(0xffffffffu, w, lane)};
+    }
+    __device__ __forceinline__ float scale() const { return __uint_as_float(w & 0xffff0000u); }
+    __device__ __forceinline__ uint32_t zero() const { return w & 0xffffu; }
+};
+template <>
+struct ScaleZero<float> {
+    float s;
+    uint32_t z;
+    __device__ __forceinline__ void load(const float *sp, const uint8_t *zp) {
+        s = __ldg(sp);
+        z = zp ? __ldg(zp) & 15u : 8u;
+    }
+    __device__ __forceinline__ ScaleZero from(int lane) const {
+        return ScaleZero{__shfl_sync(0xffffffffu, s, lane), __shfl_sync(0xffffffffu, z, lane)};
+    }
+    __device__ __forceinline__ float scale() const { return s; }
+    __device__ __forceinline__ uint32_t zero() const { return z; }
+};
+
+// x 2^e, where 2^e alone may be out of range.
+__device__ __forceinline__ float times_power(float x, int e) {
+    const int a = e / 2, b = e - a;
+    return x * __int_as_float((a + 127) << 23) * __int_as_float((b + 127) << 23);
 }
-__device__ __forceinline__ float load_scale(const float *p) { return __ldg(p); }
 
 // U: elements of k whose sums share a scale (32, 64 or 128).  wk warps of a block
 // share a tile's k.  K is laid out whole, or where it does not fit (then NT is 1)
@@ -105,13 +150,15 @@ template <int U, int NT, int MT, typename ScaleT>
 __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadParams p, int wk, int stage_k) {
     extern __shared__ __align__(16) uint4 smem4[];
     constexpr int W = U / 32;                        // words of a unit in a lane
-    constexpr int kPf = NT == 1 ? (U == 32 ? 3 : 4) : (NT == 2 ? 3 : 2);    // 128-k steps in flight
+    constexpr int kUnits = 4 / W;                    // units of a 128-k step
+    constexpr int kPf = MT == 2 ? 2 : (NT < 4 ? 4 : 2);       // steps in flight; divides 4
     constexpr int kRows = 16 * MT, kCols = 8 * NT;
+    __shared__ int power[kCols];                     // of each hidden row
     float *part = reinterpret_cast<float *>(smem4 + (size_t)NT * stage_k);      // [warps][kCols][kRows]
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int g = lane >> 2, tig = lane & 3;
     const int32_t V = p.head.V, K = p.head.K;
-    const int64_t groups = K / p.head.group;
+    const int groups = K / p.head.group;
     // a 128-k step's group, where groups are longer: step / (group / 128)
     const uint32_t long_group = U == 128 && p.head.group > 128 ? 0xffffffffu / (p.head.group / 128) + 1 : 0;
     const int64_t n_tiles = ((int64_t)V + kRows - 1) / kRows;
@@ -124,17 +171,42 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
         const int n0 = (int)(work % n_cols) * kCols;
         const int64_t t0 = work / n_cols * per, tile = t0 + wid / wk;
         const bool live = tile < n_tiles;
-        const uint8_t *wq[MT][2], *wz[MT][2];        // the lane's rows: weights, zeros,
-        const ScaleT *ws[MT][2];                     // scales
+        // the tile's weights, scales and zeros, and where the lane's rows begin in them
+        const int64_t v0 = min(tile * kRows, (int64_t)V - 1);
+        const uint8_t *tile_q = p.head.q + v0 * (K / 2);
+        const ScaleT *tile_s = reinterpret_cast<const ScaleT *>(p.head.scales) + v0 * groups;
+        const uint8_t *tile_z = p.head.zeros ? p.head.zeros + v0 * groups : nullptr;
+        uint32_t row_q[MT][2], row_s[MT][2];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int64_t row = min(tile * kRows + i * 16 + j * 8 + g, (int64_t)V - 1);
-                wq[i][j] = p.head.q + row * (K / 2) + tig * 16;
-                ws[i][j] = reinterpret_cast<const ScaleT *>(p.head.scales) + row * groups;
-                wz[i][j] = p.head.zeros + (p.head.zeros ? row * groups : 0);
+                const uint32_t row = min((int64_t)(i * 16 + j * 8 + g), V - 1 - v0);
+                row_q[i][j] = row * (uint32_t)(K / 2);
+                row_s[i][j] = row * (uint32_t)groups;
             }
+        if (laid_n0 != n0) {
+            // the power of two of each hidden row, from its largest finite element
+            __syncthreads();
+            for (int n = wid; n < kCols; n += kHeadWarps) {
+                uint32_t top = 0;
+                if (n0 + n < p.n_rows)
+                    for (int i = lane; i < K / 8; i += 32) {
+                        const uint4 h = __ldg(reinterpret_cast<const uint4 *>(
+                                                  p.hidden + (int64_t)(n0 + n) * p.hidden_ld) + i);
+                        const uint32_t x[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t lo = x[j] & 0x7fffu, hi = x[j] >> 16 & 0x7fffu;
+                            if (lo < 0x7f80u) top = max(top, lo);
+                            if (hi < 0x7f80u) top = max(top, hi);
+                        }
+                    }
+                top = __reduce_max_sync(0xffffffffu, top);
+                if (lane == 0) power[n] = top ? 14 + 127 - max(1, (int)(top >> 7)) : 0;
+            }
+            __syncthreads();
+        }
         float total[MT][NT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -163,36 +235,45 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
                         at = u * W + in % W;
                     }
                     // pairs (0, 4), (1, 5), (2, 6), (3, 7)
+                    const int e = power[n];
+                    auto pair = [&](uint32_t lo, uint32_t hi) {
+                        return h2_bits(__floats2half2_rn(times_power(__uint_as_float(lo), e),
+                                                         times_power(__uint_as_float(hi), e)));
+                    };
                     smem4[(size_t)(n / 8) * kn + at * 32 + (n % 8) * 4 + tg] =
-                        make_uint4(__byte_perm(h.x, h.z, 0x5410), __byte_perm(h.x, h.z, 0x7632),
-                                   __byte_perm(h.y, h.w, 0x5410), __byte_perm(h.y, h.w, 0x7632));
+                        make_uint4(pair(h.x << 16, h.z << 16), pair(h.x & 0xffff0000u, h.z & 0xffff0000u),
+                                   pair(h.y << 16, h.w << 16), pair(h.y & 0xffff0000u, h.w & 0xffff0000u));
                 }
                 __syncthreads();
             }
             if (!live) continue;
-            // the sums of one unit from the lane's words of it
-            auto unit = [&](const uint32_t *(&a)[MT], const uint32_t *(&b)[MT], int at, const float (&s)[MT][2],
-                            const uint32_t (&z)[MT][2]) {
+            // adds the sums of one unit, from the lane's words of it
+            auto unit = [&](const uint32_t *(&a)[MT], const uint32_t *(&b)[MT], int at,
+                            const ScaleZero<ScaleT> (&sz)[MT][2]) {
                 float c[MT][NT][4];
+                uint32_t z1[MT][2], z16[MT][2];
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
+                for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        z1[i][j] = sz[i][j].zero() * 0x10001u + 0xe400e400u;
+                        z16[i][j] = sz[i][j].zero() * 0x100010u + 0xd400d400u;
+                    }
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) c[i][n][j] = 0.f;
+                }
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     uint4 h[NT];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) h[n] = smem4[(size_t)n * kn + (at + w) * 32 + lane];
+                    for (int n = 0; n < NT; ++n) h[n] = smem4[n * kn + (at + w) * 32 + lane];
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         uint32_t x[4], y[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            x[j] = weight_pair(a[i][w], j, z[i][0]);
-                            y[j] = weight_pair(b[i][w], j, z[i][1]);
-                        }
+                        unpack(a[i][w], z1[i][0], z16[i][0], x);
+                        unpack(b[i][w], z1[i][1], z16[i][1], y);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             mma16816(c[i][n], x[0], y[0], x[1], y[1], h[n].x, h[n].y);
@@ -206,111 +287,108 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            total[i][n][j] = fmaf(s[i][j >> 1], c[i][n][j], total[i][n][j]);
+                            total[i][n][j] = fmaf(sz[i][j >> 1].scale(), c[i][n][j], total[i][n][j]);
             };
-            // of unit u, counted from k = 0
-            auto scales_of = [&](uint32_t u, float (&s)[MT][2], uint32_t (&z)[MT][2]) {
+            // the scale and zero of unit u, counted from k = 0
+            auto scale_zero = [&](ScaleZero<ScaleT> &sz, int i, int j, uint32_t u) {
                 if (U == 128 && long_group) u = __umulhi(u, long_group);
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        s[i][j] = load_scale(ws[i][j] + u);
-                        z[i][j] = p.head.zeros ? __ldg(wz[i][j] + u) & 15u : 8u;
-                    }
+                u += row_s[i][j];
+                sz.load(tile_s + u, tile_z ? tile_z + u : nullptr);
             };
-            const int n_step = kn / 128;
-            uint4 buf[kPf][MT][2];
-            float sc[4 / W][MT][2];                  // the next step's
-            uint32_t ze[4 / W][MT][2];
-            auto fetch_scales = [&](int st) {
-                if (st >= n_step) return;
+            // this warp's steps: a run, in rounds of four.  Lane `tig` of a quad holds
+            // the scales of the round's step `tig`.
+            const int n_step = kn / 128, s0 = n_step * kw / wk, s1 = n_step * (kw + 1) / wk;
+            if (s0 < s1) {
+                uint32_t buf[kPf][MT][2][4];
+                ScaleZero<ScaleT> held[kUnits][MT][2], next[kUnits][MT][2];
+                // past the end the last step is read again
+                auto fetch = [&](int st, int f) {
+                    st = min(st, s1 - 1);
 #pragma unroll
-                for (int u = 0; u < 4 / W; ++u) scales_of(ks / U + st * (4 / W) + u, sc[u], ze[u]);
-            };
-            auto fetch = [&](int st, int f) {
-                if (st >= n_step) return;
+                    for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
+                        for (int j = 0; j < 2; ++j)
+                        {
+                            const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(
+                                tile_q + (row_q[i][j] + (uint32_t)(ks / 2 + st * 64 + tig * 16))));
+                            buf[f][i][j][0] = x.x;
+                            buf[f][i][j][1] = x.y;
+                            buf[f][i][j][2] = x.z;
+                            buf[f][i][j][3] = x.w;
+                        }
+                };
+                auto fetch_scales = [&](int st) {
+                    st = ks / 128 + min(st + tig, s1 - 1);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        buf[f][i][j] = __ldcs(reinterpret_cast<const uint4 *>(wq[i][j] + ks / 2) + st * 4);
-            };
-#pragma unroll
-            for (int f = 0; f < kPf; ++f) fetch(kw + f * wk, f);
-            fetch_scales(kw);
-            for (int st = kw; st < n_step; st += kPf * wk) {
-#pragma unroll
-                for (int f = 0; f < kPf; ++f) {
-                    const int now = st + f * wk;
-                    if (now < n_step) {
-                        uint32_t q[MT][2][4];
-                        float s[4 / W][MT][2];
-                        uint32_t z[4 / W][MT][2];
+                    for (int u = 0; u < kUnits; ++u)
 #pragma unroll
                         for (int i = 0; i < MT; ++i)
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                q[i][j][0] = buf[f][i][j].x;
-                                q[i][j][1] = buf[f][i][j].y;
-                                q[i][j][2] = buf[f][i][j].z;
-                                q[i][j][3] = buf[f][i][j].w;
+                            for (int j = 0; j < 2; ++j) scale_zero(next[u][i][j], i, j, st * kUnits + u);
+                };
+                fetch_scales(s0);
 #pragma unroll
-                                for (int u = 0; u < 4 / W; ++u) {
-                                    s[u][i][j] = sc[u][i][j];
-                                    z[u][i][j] = 0x43004300u | ze[u][i][j] * 0x10001u;
-                                }
-                            }
-                        fetch(now + kPf * wk, f);
-                        fetch_scales(now + wk);
+                for (int f = 0; f < kPf; ++f) fetch(s0 + f, f);
+                for (int st = s0; st < s1; st += 4) {
+#pragma unroll
+                    for (int u = 0; u < kUnits; ++u)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) held[u][i][j] = next[u][i][j];
+                    if (st + 4 < s1) fetch_scales(st + 4);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        if (st + f >= s1) break;
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            spread<U>(q[i][0], tig);
-                            spread<U>(q[i][1], tig);
+                            spread<U>(buf[f % kPf][i][0], tig);
+                            spread<U>(buf[f % kPf][i][1], tig);
                         }
 #pragma unroll
-                        for (int u = 0; u < 4 / W; ++u) {
+                        for (int u = 0; u < kUnits; ++u) {
                             const uint32_t *a[MT], *b[MT];
+                            ScaleZero<ScaleT> sz[MT][2];
 #pragma unroll
                             for (int i = 0; i < MT; ++i) {
-                                a[i] = &q[i][0][u * W];
-                                b[i] = &q[i][1][u * W];
+                                a[i] = &buf[f % kPf][i][0][u * W];
+                                b[i] = &buf[f % kPf][i][1][u * W];
+                                sz[i][0] = held[u][i][0].from((lane & ~3) + f);
+                                sz[i][1] = held[u][i][1].from((lane & ~3) + f);
                             }
-                            unit(a, b, now * 4 + u * W, s[u], z[u]);
+                            unit(a, b, (st + f) * 4 + u * W, sz);
                         }
+                        fetch(st + f + kPf, f % kPf);
                     }
                 }
             }
             // what is left of k after whole steps: units, by the words of the unit
             if constexpr (U < 128) {
-                for (int u = n_step * (4 / W) + kw; u < kn / U; u += wk) {
+                for (int u = n_step * kUnits + kw; u < kn / U; u += wk) {
                     uint32_t q[MT][2][W];
                     const uint32_t *a[MT], *b[MT];
+                    ScaleZero<ScaleT> sz[MT][2];
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
+                        for (int j = 0; j < 2; ++j) {
 #pragma unroll
                             for (int w = 0; w < W; ++w)
                                 q[i][j][w] = __ldg(reinterpret_cast<const uint32_t *>(
-                                    wq[i][j] - tig * 16 + ks / 2 + u * (U / 2) + tig * (U / 8)) + w);
+                                    tile_q + (row_q[i][j] + (uint32_t)(ks / 2 + u * (U / 2) + tig * (U / 8)))) + w);
+                            scale_zero(sz[i][j], i, j, ks / U + u);
+                        }
                         a[i] = q[i][0];
                         b[i] = q[i][1];
                     }
-                    float s[MT][2];
-                    uint32_t z[MT][2];
-                    scales_of(ks / U + u, s, z);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) z[i][j] = 0x43004300u | z[i][j] * 0x10001u;
-                    unit(a, b, u * W, s, z);
+                    unit(a, b, u * W, sz);
                 }
             }
         }
         auto store = [&](int n, int64_t v, float x) {
             if (v >= V || n0 + n >= p.n_rows) return;
             const int64_t at = (int64_t)(n0 + n) * p.ld + v;
+            x = times_power(x, -power[n]);
             if (p.dtype == PS_BF16)
                 reinterpret_cast<__nv_bfloat16 *>(p.logits)[at] = __float2bfloat16_rn(x);
             else
@@ -386,8 +464,8 @@ template <int U, typename ScaleT>
 cudaError_t launch_n(const HeadParams &p, int sms, cudaStream_t stream) {
     const int64_t fits = kHeadSmem / ((int64_t)p.head.K * 16);
     if (p.n_rows > 16 && fits >= 4) return launch<U, 4, 1, ScaleT>(p, sms, stream);
-    if (p.n_rows > 8 && fits >= 2) return launch<U, 2, 1, ScaleT>(p, sms, stream);
-    return launch<U, 1, 1, ScaleT>(p, sms, stream);
+    if (p.n_rows > 8 && fits >= 2) return launch<U, 2, U == 128 ? 2 : 1, ScaleT>(p, sms, stream);
+    return launch<U, 1, U >= 64 ? 2 : 1, ScaleT>(p, sms, stream);
 }
 
 template <int U>
