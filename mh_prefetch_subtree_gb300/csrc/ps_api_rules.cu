@@ -51,11 +51,6 @@ ScoreWs score_ws(const ps_subtree_batch *b) {
     return w;
 }
 
-int32_t slices_of(int32_t V, int32_t dtype) {
-    const int32_t s = rules_slice_ids(dtype);
-    return (int32_t)(((int64_t)V + s - 1) / s);
-}
-
 }  // namespace
 
 extern "C" {
@@ -91,7 +86,7 @@ ps_status ps_process_rows(const ps_logit_rules *rules, int32_t V, int32_t dtype,
     p.out = (uint8_t *)out;
     p.ld_bytes = ld * esz;
     p.out_ld_bytes = out_ld * esz;
-    p.n_slices = slices_of(V, dtype);
+    p.row_bytes = ((int64_t)V * esz + 15) / 16 * 16;
     return map_cuda(launch_process_rows(p, dtype, sms, (cudaStream_t)cuda_stream));
 }
 

@@ -34,8 +34,6 @@
 namespace ps {
 namespace {
 
-constexpr int kHeadWarps = 16;
-constexpr int kHeadThreads = kHeadWarps * 32;
 constexpr int kHeadSmem = 200 * 1024;  // for hidden rows
 constexpr int kMaxStageK = 8192;       // hidden elements laid out at a time, when not all fit
 
@@ -146,12 +144,13 @@ __device__ __forceinline__ float times_power(float x, int e) {
 // U: elements of k whose sums share a scale (32, 64 or 128).  wk warps of a block
 // share a tile's k.  K is laid out whole, or where it does not fit (then NT is 1)
 // in parts that all warps of the block work on together.
-template <int U, int NT, int MT, typename ScaleT>
-__global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadParams p, int wk, int stage_k) {
+template <int U, int NT, int MT, int WARPS, typename ScaleT>
+__global__ void __launch_bounds__(WARPS * 32, 1) head_rows_kernel(const HeadParams p, int wk, int stage_k) {
     extern __shared__ __align__(16) uint4 smem4[];
+    constexpr int kHeadWarps = WARPS, kHeadThreads = WARPS * 32;
     constexpr int W = U / 32;                        // words of a unit in a lane
     constexpr int kUnits = 4 / W;                    // units of a 128-k step
-    constexpr int kPf = MT == 2 ? 2 : (NT < 4 ? 4 : 2);       // steps in flight; divides 4
+    constexpr int kPf = MT * WARPS == 32 ? 2 : 4;     // steps in flight; divides 4
     constexpr int kRows = 16 * MT, kCols = 8 * NT;
     __shared__ int power[kCols];                     // of each hidden row
     float *part = reinterpret_cast<float *>(smem4 + (size_t)NT * stage_k);      // [warps][kCols][kRows]
@@ -428,11 +427,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) head_rows_kernel(const HeadPa
 
 // Warps that share a tile's k: as few as give every warp work, and of those the
 // number that leaves the least of it over in the last round.
-int split_k(int64_t tiles, int64_t cols, int sms, int steps) {
+int split_k(int64_t tiles, int64_t cols, int sms, int steps, int warps) {
     int best = 1;
     double least = 1e30;
-    for (int wk = 1; wk <= kHeadWarps && (wk == 1 || wk <= steps); wk *= 2) {
-        const int64_t per = kHeadWarps / wk, work = (tiles + per - 1) / per * cols;
+    for (int wk = 1; wk <= warps && warps % wk == 0 && (wk == 1 || wk <= steps); wk *= 2) {
+        const int64_t per = warps / wk, work = (tiles + per - 1) / per * cols;
         const double rounds = (double)((work + sms - 1) / sms) / wk;
         if (rounds < 0.9 * least) {
             least = rounds;
@@ -442,30 +441,33 @@ int split_k(int64_t tiles, int64_t cols, int sms, int steps) {
     return best;
 }
 
-template <int U, int NT, int MT, typename ScaleT>
+template <int U, int NT, int MT, int WARPS, typename ScaleT>
 cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     const int K = p.head.K;
     const int stage_k = (int64_t)NT * K * 16 <= kHeadSmem ? K : kMaxStageK;
     const int64_t tiles = ((int64_t)p.head.V + 16 * MT - 1) / (16 * MT);
     const int64_t cols = ((int64_t)p.n_rows + 8 * NT - 1) / (8 * NT);
-    const int wk = split_k(tiles, cols, sms, K / (U < 128 ? U : 128));
-    const int smem = NT * stage_k * 16 + (wk > 1 ? kHeadWarps * 16 * MT * 8 * NT * 4 : 0);
-    cudaError_t e = cudaFuncSetAttribute(head_rows_kernel<U, NT, MT, ScaleT>,
+    const int wk = split_k(tiles, cols, sms, K / 128, WARPS);
+    const int smem = NT * stage_k * 16 + (wk > 1 ? WARPS * 16 * MT * 8 * NT * 4 : 0);
+    cudaError_t e = cudaFuncSetAttribute(head_rows_kernel<U, NT, MT, WARPS, ScaleT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int64_t per = kHeadWarps / wk, work = (tiles + per - 1) / per * cols;
-    head_rows_kernel<U, NT, MT, ScaleT>
-        <<<(unsigned)(work < sms ? work : sms), kHeadThreads, smem, stream>>>(p, wk, stage_k);
+    const int64_t per = WARPS / wk, work = (tiles + per - 1) / per * cols;
+    head_rows_kernel<U, NT, MT, WARPS, ScaleT>
+        <<<(unsigned)(work < sms ? work : sms), WARPS * 32, smem, stream>>>(p, wk, stage_k);
     return cudaGetLastError();
 }
 
-// Hidden rows of a block: 8, 16 or 32, as many as there are and as fit.
+// Hidden rows of a block: 8, 16 or 32, as many as there are and as fit.  With 8, a
+// warp takes 32 vocabulary rows (1 row of 151936 x 4096: 74 us, with 16: 96); with more
+// there are not the registers (16 rows: 105 us with 32, 98 with 16).  12 warps instead of
+// 16 pay with 32 hidden rows only (64 rows of 262144 x 2048: 254 and 279 us).
 template <int U, typename ScaleT>
 cudaError_t launch_n(const HeadParams &p, int sms, cudaStream_t stream) {
     const int64_t fits = kHeadSmem / ((int64_t)p.head.K * 16);
-    if (p.n_rows > 16 && fits >= 4) return launch<U, 4, 1, ScaleT>(p, sms, stream);
-    if (p.n_rows > 8 && fits >= 2) return launch<U, 2, U == 128 ? 2 : 1, ScaleT>(p, sms, stream);
-    return launch<U, 1, U >= 64 ? 2 : 1, ScaleT>(p, sms, stream);
+    if (p.n_rows > 16 && fits >= 4) return launch<U, 4, 1, 12, ScaleT>(p, sms, stream);
+    if (p.n_rows > 8 && fits >= 2) return launch<U, 2, 1, 16, ScaleT>(p, sms, stream);
+    return launch<U, 1, U >= 64 ? 2 : 1, 16, ScaleT>(p, sms, stream);
 }
 
 template <int U>

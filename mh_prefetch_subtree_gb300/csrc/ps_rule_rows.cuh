@@ -102,8 +102,8 @@ struct RuleSmem {
     RowDesc desc[RING];
     RowRules rules[RING];
     uint64_t mask_ids[kMaskCache];                   // a mask and slice, and its ids there
-    // a stage is full (producer and copies), patched, and read; free: may be filled
-    uint64_t full[RING], patched[RING], empty[RING], free[RING];
+    // a stage is full (producer and copies), patched, and finished with
+    uint64_t full[RING], patched[RING], empty[RING];
     uint64_t sync;                                   // the patchers' own barrier
     int32_t bad[2];                                  // of a rebuild, by its parity
 };
@@ -138,6 +138,40 @@ struct SliceMap {
     }
 };
 
+// For each byte (bfloat16) or nibble (float32) of a mask word the 32-bit masks of a
+// 16-byte vector's words.
+template <int DT>
+constexpr int kLutSize = DT == PS_BF16 ? 256 : 16;
+template <int DT>
+__device__ __forceinline__ void fill_lut(uint4 *lut) {
+    for (int i = threadIdx.x; i < kLutSize<DT>; i += blockDim.x) {
+        uint32_t k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == PS_BF16)
+                k[j] = ((i >> (2 * j)) & 1 ? 0xffffu : 0u) | ((i >> (2 * j + 1)) & 1 ? 0xffff0000u : 0u);
+            else
+                k[j] = (i >> j) & 1 ? 0xffffffffu : 0u;
+        }
+        lut[i] = make_uint4(k[0], k[1], k[2], k[3]);
+    }
+}
+// q with `off` in the places whose bit of `bits` is 0.
+template <int DT>
+__device__ __forceinline__ uint4 masked_by(uint4 q, const uint4 *lut, uint32_t bits, uint32_t off) {
+    const uint4 k = lut[bits & (kLutSize<DT> - 1)];
+    q.x = (q.x & k.x) | (off & ~k.x);
+    q.y = (q.y & k.y) | (off & ~k.y);
+    q.z = (q.z & k.z) | (off & ~k.z);
+    q.w = (q.w & k.w) | (off & ~k.w);
+    return q;
+}
+
+// The block h of 32 ids that a lane of a warp that works on all ids takes.
+__device__ __forceinline__ uint32_t block_of(int wid, int lane, int h) {
+    return (h * 32 + lane) * kSumWarps + (wid + lane) % kSumWarps;
+}
+
 // Times that id is among tokens b .. e - 1.
 __device__ __noinline__ uint32_t recount(const int32_t *hist, int32_t b, int32_t e, int32_t id) {
     uint32_t c = 0;
@@ -169,12 +203,14 @@ struct RuleSpan {
 // A producer warp: fills stage `me` with every RING-th row.
 // SPARSE: where a row's mask leaves few of the slice's ids, only the 16-byte
 // vectors that hold one are copied.
-template <int DT, int NB, int RING, bool SPARSE>
+// done(row, slice): called once the consumers have finished the stage's row, before
+// the stage is filled again.
+template <int DT, int NB, int RING, bool SPARSE, typename Done>
 __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const RulesParams &p,
                                               const RuleCut &cut, const uint8_t *logits,
                                               int64_t ld_bytes, int64_t row_bytes,
                                               const int64_t *row_index, int64_t n_logit_rows,
-                                              const int32_t *tokens, uint64_t *free_bars) {
+                                              const int32_t *tokens, Done done) {
     using Smem = RuleSmem<DT, NB, RING>;
     constexpr int kEsz = Smem::kEsz;
     constexpr int kWpl = Smem::kBlocks / 32;               // mask words of a lane
@@ -196,7 +232,8 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
     int32_t win = -64, win_tok = 0;                        // 32 tokens of its history
 
     int64_t t = span.t0 + me;
-    int64_t r = t % span.rows;
+    int64_t r = t % span.rows, r_before = 0;
+    int32_t slice_before = 0;
     SliceMap map(cut, p.V, (int32_t)(t / span.rows));
     for (; t < span.t1; t += RING) {
         // the window holds r and the row before
@@ -270,10 +307,15 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
         const int64_t step = t - span.t0;
         const int s = me;
         const uint32_t lap = (uint32_t)(step / RING);
-        if (lap > 0 && !mbar_wait_bounded(&free_bars[s], (lap - 1) & 1u, kRuleWaitNs)) {
-            if (lane == 0) set_status(p.status, PS_DEV_TIMEOUT);
-            break;
+        if (lap > 0) {
+            if (!mbar_wait_bounded(&sm.empty[s], (lap - 1) & 1u, kRuleWaitNs)) {
+                if (lane == 0) set_status(p.status, PS_DEV_TIMEOUT);
+                break;
+            }
+            done(s, r_before, slice_before);
         }
+        r_before = r;
+        slice_before = map.slice;
         // logits and mask
         const uint32_t bytes = (uint32_t)(map.nid * kEsz + 15) / 16 * 16;
         const uint8_t *from = logits + src * ld_bytes;
@@ -371,11 +413,13 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
             base = -1;
         }
     }
-    // copies in flight land before the block's memory goes
-    t -= RING;                                             // the last row that was filled
+    // the last row that was filled: its copies land before the block's memory goes
+    t -= RING;
     if (t >= span.t0 && t < span.t1) {
-        const int64_t step = t - span.t0;
-        mbar_wait_bounded(&sm.full[me], (uint32_t)(step / RING) & 1u, kRuleDrainNs);
+        const uint32_t odd = (uint32_t)((t - span.t0) / RING) & 1u;
+        if (mbar_wait_bounded(&sm.full[me], odd, kRuleDrainNs) &&
+            mbar_wait_bounded(&sm.empty[me], odd, kRuleWaitNs))
+            done(me, r_before, slice_before);
     }
 }
 
@@ -610,14 +654,13 @@ struct RuleWalk {
 };
 
 template <typename Smem, int RING>
-__device__ __forceinline__ void rule_smem_init(Smem &sm, int free_count) {
+__device__ __forceinline__ void rule_smem_init(Smem &sm) {
     for (int i = threadIdx.x; i < kMaskCache; i += blockDim.x) sm.mask_ids[i] = 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < RING; ++s) {
             mbar_init(&sm.full[s], 33);               // the producer's lanes, and once more
             mbar_init(&sm.patched[s], kPatchWarps);
             mbar_init(&sm.empty[s], kSumWarps);
-            mbar_init(&sm.free[s], free_count);
         }
         mbar_init(&sm.sync, kPatchWarps);
         fence_mbar_init();

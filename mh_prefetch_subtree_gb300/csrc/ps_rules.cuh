@@ -19,7 +19,7 @@ struct ProcessParams {
     uint8_t *out;               // may be logits itself
     int64_t ld_bytes;
     int64_t out_ld_bytes;
-    int32_t n_slices;
+    int64_t row_bytes;          // of the V logits, rounded up to 16
 };
 
 // How the vocabulary is cut for the kernels that stream rows: into segments of
@@ -51,8 +51,6 @@ struct ScoreRulesParams {
 cudaError_t launch_process_rows(const ProcessParams &p, int32_t dtype, int sms,
                                 cudaStream_t stream);
 cudaError_t launch_score_rules(const ScoreRulesParams &p, int sms, cudaStream_t stream);
-// Ids of a vocabulary slice for rows of `dtype`.
-int32_t rules_slice_ids(int32_t dtype);
 
 #ifdef __CUDACC__
 namespace {
@@ -183,11 +181,13 @@ __device__ __forceinline__ bool is_biased(const SliceTable &t, uint32_t o) {
     return (t.biased[o >> 5] >> (o & 31)) & 1u;
 }
 
-// The penalised logit of an id with count word c.
-__device__ __forceinline__ float penalised(float l, uint32_t c, const RowRules &w) {
-    if (c & kSeen) l = l > 0.f ? l / w.rho : l * w.rho;
+// The processed logit of an id with count word c, in the order of operations of
+// the kernels that stream rows: a factor by sign, then one summand.
+__device__ __forceinline__ float penalised(float l, uint32_t c, const RowRules &w, float bias) {
     const uint32_t n = c & ~kSeen;
-    return l - w.freq * (float)n - (n ? w.pres : 0.f);
+    float f = 1.f;
+    if (c & kSeen) f = l > 0.f ? 1.f / w.rho : w.rho;
+    return fmaf(l, f, bias - (w.freq * (float)n + (n ? w.pres : 0.f)));
 }
 
 __device__ __forceinline__ bool mask_allows(const uint32_t *mask, int32_t v) {

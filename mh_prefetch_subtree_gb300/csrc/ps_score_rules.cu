@@ -33,7 +33,7 @@ constexpr float kLeast = 8.673617379884035e-19f;     // 2^-60
 
 template <int DT>
 struct ScoreSmem : RuleSmem<DT, DT == PS_BF16 ? 2 : 1, kRing> {
-    uint4 lut[DT == PS_BF16 ? 256 : 16];             // mask bits -> which words stay
+    uint4 lut[kLutSize<DT>];                         // mask bits -> which words stay
     uint4 off[8];                                    // a block that does not count
     // processed logits of the first touched ids of each patcher, and how many
     float touched[kRing][kPatchWarps][kTouched];
@@ -63,11 +63,6 @@ __device__ __forceinline__ float tau_term(float y, float e, float g) {
     else if constexpr (NP == 2) return e * e;
     else if constexpr (NP == 4) return (e * e) * (e * e);
     else return ((e * e) * (e * e)) * ((e * e) * (e * e));
-}
-
-// The lane's block h in the slice.
-__device__ __forceinline__ uint32_t block_of(int wid, int lane, int h) {
-    return (h * 32 + lane) * kSumWarps + (wid + lane) % kSumWarps;
 }
 
 // Sums relative to a reference, by lane.
@@ -104,16 +99,6 @@ struct LaneIds {
     int first;                  // vector to begin with
     uint32_t ma, mb;            // its bits at the bottom
 };
-
-template <int DT>
-__device__ __forceinline__ uint4 masked_by(uint4 q, const uint4 *lut, uint32_t bits, uint32_t off) {
-    const uint4 k = lut[bits & (DT == PS_BF16 ? 0xffu : 15u)];
-    q.x = (q.x & k.x) | (off & ~k.x);
-    q.y = (q.y & k.y) | (off & ~k.y);
-    q.z = (q.z & k.z) | (off & ~k.z);
-    q.w = (q.w & k.w) | (off & ~k.w);
-    return q;
-}
 
 // Calls f(vector, vector) for the lane's pairs of vectors, those of b after those
 // of a.  A rolled loop: the eight vectors in one run of code would not fit the
@@ -325,25 +310,15 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const float g = p.rows.g;
 
-    for (int i = threadIdx.x; i < (DT == PS_BF16 ? 256 : 16); i += blockDim.x) {
-        uint32_t k[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == PS_BF16)
-                k[j] = ((i >> (2 * j)) & 1 ? 0xffffu : 0u) | ((i >> (2 * j + 1)) & 1 ? 0xffff0000u : 0u);
-            else
-                k[j] = (i >> j) & 1 ? 0xffffffffu : 0u;
-        }
-        sm.lut[i] = make_uint4(k[0], k[1], k[2], k[3]);
-    }
+    fill_lut<DT>(sm.lut);
     if (threadIdx.x < kBv) sm.off[threadIdx.x] = make_uint4(kOff, kOff, kOff, kOff);
-    rule_smem_init<Smem, kRing>(sm, 1);
+    rule_smem_init<Smem, kRing>(sm);
     __syncthreads();
 
     if (wid >= kFirstProducer) {
         rule_producer<DT, kNb, kRing, true>(sm, p.r, p.cut, p.rows.logits, p.rows.ld_bytes,
                                             p.rows.row_bytes, p.rows.row_index, p.rows.n_logit_rows,
-                                            p.rows.tokens, sm.empty);
+                                            p.rows.tokens, [](int, int64_t, int32_t) {});
         return;
     }
     if (wid >= kSumWarps) {
