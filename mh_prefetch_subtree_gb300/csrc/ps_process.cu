@@ -141,9 +141,12 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) process_rows_kernel(
     int s = 0;
     uint32_t lap = 0;
     const uint32_t first = block_of(wid, lane, 0);
+    uint32_t fills = 0;
     for (int64_t t = span.t0; t < span.t1; ++t) {
-        if (!mbar_wait_bounded(&sm.full[s], lap & 1u, kRuleWaitNs) ||
-            !mbar_wait_bounded(&sm.patched[s], lap & 1u, kRuleWaitNs)) {
+        bool ok = mbar_wait_bounded(&sm.full[s], lap & 1u, kRuleWaitNs);
+        if (ok && (sm.desc[s].flags & kDescRebuild))
+            ok = rule_tables(sm, SliceMap(cut, p.r.V, slice), sm.rules[s], fills++) != nullptr;
+        if (!ok || !mbar_wait_bounded(&sm.patched[s], lap & 1u, kRuleWaitNs)) {
             if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
             return;
         }

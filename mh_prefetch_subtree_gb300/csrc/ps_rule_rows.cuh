@@ -21,8 +21,8 @@
 // while it is short.  Blocks of 32 ids (one mask word) are dealt to them in turn:
 // ids of common tokens lie close together, so a warp that owned a long run of ids
 // could hold most of a history.  A new token costs a few instructions in the one
-// warp that owns it.  Where the sequence changes, the patchers read the whole
-// history together.
+// warp that owns it.  Where the sequence changes, all warps but the producers read
+// the whole history together.
 #pragma once
 
 #include "ps_row_sums.cuh"
@@ -34,6 +34,7 @@ namespace {
 constexpr int kSumWarps = 12;                        // work on all ids
 constexpr int kPatchWarps = 4;
 constexpr int kPatchThreads = kPatchWarps * 32;
+constexpr int kCountThreads = (kSumWarps + kPatchWarps) * 32;
 constexpr int kFirstProducer = kSumWarps + kPatchWarps;
 // One producer a stage: a stage's phases then are one warp's to wait for, in
 // order.  (With more producers than stages one could wait two phases ahead, which
@@ -104,7 +105,7 @@ struct RuleSmem {
     uint64_t mask_ids[kMaskCache];                   // a mask and slice, and its ids there
     // a stage is full (producer and copies), patched, and finished with
     uint64_t full[RING], patched[RING], empty[RING];
-    uint64_t sync;                                   // the patchers' own barrier
+    uint64_t sync;                                   // all warps but the producers
     int32_t bad[2];                                  // of a rebuild, by its parity
 };
 
@@ -423,6 +424,82 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
     }
 }
 
+// Waits for all warps but the producers, for the n-th time; false when they do not
+// come.
+template <typename Smem>
+__device__ __forceinline__ bool rule_meet(Smem &sm, uint32_t n) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.sync);
+    return mbar_wait_bounded(&sm.sync, n & 1u, kRuleWaitNs);
+}
+
+template <typename Smem>
+__device__ __forceinline__ void count_token(Smem &sm, const SliceMap &map, int32_t id, bool made, bool fits,
+                                            int32_t *bad_word) {
+    if (id < 0 || id >= map.V) {
+        atomicOr(bad_word, PS_DEV_BAD_TOKEN);
+        return;
+    }
+    const int32_t d = map.local(id);
+    if (d < 0) return;
+    atomicOr(&sm.seen[d >> 5], 1u << (d & 31));
+    if (!made) return;
+    uint32_t *word = reinterpret_cast<uint32_t *>(&sm.count[d & ~1]);
+    const int sh = (d & 1) * 16;
+    if (fits) {
+        atomicAdd(word, 1u << sh);
+    } else {
+        uint32_t old = *reinterpret_cast<volatile uint32_t *>(word), was;
+        do {
+            was = old;
+            if (((was >> sh) & 0xffffu) == kCountFull) break;
+            old = atomicCAS(word, was, was + (1u << sh));
+        } while (old != was);
+    }
+}
+
+// Counts and bit sets of a history, made by all warps but the producers together,
+// for the k-th time in this block.  Where the status bits of the history and the
+// biases are; nullptr on a timeout.
+template <typename Smem>
+__device__ __noinline__ const int32_t *rule_tables(Smem &sm, SliceMap map, const RowRules &w, uint32_t k) {
+    const int tid = threadIdx.x;
+    const int32_t blocks = (map.nid + kBlockIds - 1) / kBlockIds, len = w.len, prompt = w.prompt;
+    const int32_t *hist = w.hist;
+    // a warp may still read the word of the time before
+    int32_t *bad_word = &sm.bad[k & 1];
+    if (tid == 0) *bad_word = 0;
+    if (!rule_meet(sm, 3 * k)) return nullptr;      // the patchers are done with the tables
+    for (int i = tid; i < blocks * kBlockIds / 8; i += kCountThreads)
+        reinterpret_cast<uint4 *>(sm.count)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < blocks; i += kCountThreads) sm.seen[i] = sm.biased[i] = 0;
+    if (!rule_meet(sm, 3 * k + 1)) return nullptr;
+    const bool fits = len - max(0, min(prompt, len)) < (int32_t)kCountFull;
+    for (int b = 0; b < len; b += kCountThreads * 4) {
+        int32_t id[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = b + j * kCountThreads + tid;
+            id[j] = i < len ? __ldg(hist + i) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = b + j * kCountThreads + tid;
+            if (i < len) count_token(sm, map, id[j], i >= prompt, fits, bad_word);
+        }
+    }
+    for (int i = tid; i < w.n_bias; i += kCountThreads) {
+        const int32_t id = __ldg(w.bias_ids + i);
+        if (id < 0 || id >= map.V || (i > 0 && id <= __ldg(w.bias_ids + i - 1))) {
+            atomicOr(bad_word, PS_DEV_BAD_RULES);
+            continue;
+        }
+        const int32_t d = map.local(id);
+        if (d >= 0) atomicOr(&sm.biased[d >> 5], 1u << (d & 31));
+    }
+    return rule_meet(sm, 3 * k + 2) ? bad_word : nullptr;
+}
+
 // A patching warp's view of the rules.  The same in all lanes unless said
 // otherwise.
 template <typename Smem>
@@ -435,8 +512,7 @@ struct RuleWalk {
     int32_t n_list = 0;         // touched ids; the first n_bias of the list are biased
     int32_t n_bias = 0;
     int32_t bad = 0;            // status bits of the history and the biases
-    uint32_t lap = 0;           // of the patchers' own barrier
-    uint32_t rebuilds = 0;
+    uint32_t fills = 0;         // of the tables
     RowRules w{};
     float inv_rho = 1.f;
     // by lane: entries lane, lane + 32, ... of the list (local number, kMade set:
@@ -451,15 +527,6 @@ struct RuleWalk {
     __device__ __forceinline__ bool is_biased(uint32_t d) const {
         return (sm.biased[d >> 5] >> (d & 31)) & 1u;
     }
-    // Waits for the other patchers; false when they do not come.
-    __device__ __forceinline__ bool meet() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.sync);
-        const bool ok = mbar_wait_bounded(&sm.sync, lap & 1u, kRuleWaitNs);
-        ++lap;
-        return ok;
-    }
-
     // How often id d was generated.  A count that does not fit 16 bits is taken
     // again from the history: slow, and as rare as a token that one sequence holds
     // 65535 times.
@@ -488,69 +555,15 @@ struct RuleWalk {
         }
     }
 
-    __device__ __forceinline__ void count_shared(int32_t i, int32_t id, bool fits, int32_t *bad_word) {
-        if (id < 0 || id >= p.V) {
-            atomicOr(bad_word, PS_DEV_BAD_TOKEN);
-            return;
-        }
-        const int32_t d = map.local(id);
-        if (d < 0) return;
-        atomicOr(&sm.seen[d >> 5], 1u << (d & 31));
-        if (i < w.prompt) return;
-        uint32_t *word = reinterpret_cast<uint32_t *>(&sm.count[d & ~1u]);
-        const int sh = (d & 1) * 16;
-        if (fits) {
-            atomicAdd(word, 1u << sh);
-        } else {
-            uint32_t old = *reinterpret_cast<volatile uint32_t *>(word), was;
-            do {
-                was = old;
-                if (((was >> sh) & 0xffffu) == kCountFull) break;
-                old = atomicCAS(word, was, was + (1u << sh));
-            } while (old != was);
-        }
-    }
-
     // Takes up a row's sequence with its history so far.  False on a timeout.
     __device__ __forceinline__ bool rebuild(const RowRules &from) {
-        const int tid = threadIdx.x - kSumWarps * 32;
         w = from;
         inv_rho = 1.f / w.rho;
         len = w.len;
+        const int32_t *bad_word = rule_tables(sm, map, from, fills++);
+        if (bad_word == nullptr) return false;
+        bad = *reinterpret_cast<const volatile int32_t *>(bad_word);
         const int32_t blocks = (map.nid + kBlockIds - 1) / kBlockIds;
-        // a warp may still read the word of the rebuild before
-        int32_t *bad_word = &sm.bad[rebuilds++ & 1];
-        if (tid == 0) *bad_word = 0;
-        if (!meet()) return false;                  // the others are done with the tables
-        for (int i = tid; i < blocks * kBlockIds / 8; i += kPatchThreads)
-            reinterpret_cast<uint4 *>(sm.count)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = tid; i < blocks; i += kPatchThreads) sm.seen[i] = sm.biased[i] = 0;
-        if (!meet()) return false;
-        const bool fits = w.len - max(0, min(w.prompt, w.len)) < (int32_t)kCountFull;
-        for (int b = 0; b < w.len; b += kPatchThreads * 4) {
-            int32_t id[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = b + j * kPatchThreads + tid;
-                id[j] = i < w.len ? __ldg(w.hist + i) : 0;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = b + j * kPatchThreads + tid;
-                if (i < w.len) count_shared(i, id[j], fits, bad_word);
-            }
-        }
-        for (int i = tid; i < w.n_bias; i += kPatchThreads) {
-            const int32_t id = __ldg(w.bias_ids + i);
-            if (id < 0 || id >= p.V || (i > 0 && id <= __ldg(w.bias_ids + i - 1))) {
-                atomicOr(bad_word, PS_DEV_BAD_RULES);
-                continue;
-            }
-            const int32_t d = map.local(id);
-            if (d >= 0) atomicOr(&sm.biased[d >> 5], 1u << (d & 31));
-        }
-        if (!meet()) return false;
-        bad = *reinterpret_cast<volatile int32_t *>(bad_word);
         // the list: the biased ids in the order of their list, then the others seen
         n_list = 0;
         for (int b = 0; bad == 0 && b < w.n_bias; b += 32) {
@@ -662,7 +675,7 @@ __device__ __forceinline__ void rule_smem_init(Smem &sm) {
             mbar_init(&sm.patched[s], kPatchWarps);
             mbar_init(&sm.empty[s], kSumWarps);
         }
-        mbar_init(&sm.sync, kPatchWarps);
+        mbar_init(&sm.sync, kSumWarps + kPatchWarps);
         fence_mbar_init();
     }
 }
