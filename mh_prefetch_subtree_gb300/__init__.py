@@ -325,13 +325,14 @@ def ps_process_rows(rules: PsLogitRules, logits: torch.Tensor, out: torch.Tensor
     dt = _row_dtype(logits, "logits")
     _need(out, logits.dtype, "out")
     _need(status, torch.int32, "status")
-    if logits.dim() != 2 or out.dim() != 2 or out.shape[0] != logits.shape[0]:
+    shape, out_shape = logits.shape, out.shape
+    if len(shape) != 2 or len(out_shape) != 2 or out_shape[0] != shape[0]:
         raise ValueError("logits and out must be [n_rows, ld] with the same n_rows")
-    n_rows, ld, out_ld = logits.shape[0], logits.shape[1], out.shape[1]
+    n_rows, ld = shape
     _need_rows(rules, n_rows)
-    st = lib().ps_process_rows(ctypes.byref(rules), ld if V is None else int(V), dt, n_rows,
-                               _ptr(logits), ld, _ptr(out), out_ld, _ptr(status),
-                               _stream(stream, logits))
+    st = (_lib or lib()).ps_process_rows(rules, ld if V is None else V, dt, n_rows, _ptr(logits),
+                                         ld, _ptr(out), out_shape[1], _ptr(status),
+                                         _stream(stream, logits))
     if check and st != PS_OK:
         raise PsError(st, "ps_process_rows")
     return st
@@ -352,10 +353,9 @@ def ps_score_rows_rules(batch: PsSubtreeBatch, rules: PsLogitRules, lp0: torch.T
     _need(entropy, torch.float64, "entropy", optional=True)
     _need(status, torch.int32, "status")
     _need_rows(rules, batch.n_rows)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = lib().ps_score_rows_rules(ctypes.byref(batch), ctypes.byref(rules), _ptr(lp0), _ptr(lq),
-                                   _ptr(entropy), _ptr(status), _ptr(workspace), ws_bytes,
-                                   _stream(stream, workspace))
+    st = (_lib or lib()).ps_score_rows_rules(batch, rules, _ptr(lp0), _ptr(lq), _ptr(entropy),
+                                             _ptr(status), _ptr(workspace), workspace.nbytes,
+                                             _stream(stream, workspace))
     if check and st != PS_OK:
         raise PsError(st, "ps_score_rows_rules")
     return st
@@ -367,10 +367,11 @@ def ps_head_rows(head: PsHead, hidden: torch.Tensor, logits: torch.Tensor, strea
     [n_rows, >= K] bfloat16, logits [n_rows, ld] bfloat16 or float32."""
     _need(hidden, torch.bfloat16, "hidden")
     dt = _row_dtype(logits, "logits")
-    if hidden.dim() != 2 or logits.dim() != 2 or hidden.shape[0] != logits.shape[0]:
+    shape, out_shape = hidden.shape, logits.shape
+    if len(shape) != 2 or len(out_shape) != 2 or out_shape[0] != shape[0]:
         raise ValueError("hidden and logits must be matrices with the same number of rows")
-    st = lib().ps_head_rows(ctypes.byref(head), _ptr(hidden), hidden.shape[1], hidden.shape[0],
-                            _ptr(logits), logits.shape[1], dt, _stream(stream, logits))
+    st = (_lib or lib()).ps_head_rows(head, _ptr(hidden), shape[1], shape[0], _ptr(logits),
+                                      out_shape[1], dt, _stream(stream, logits))
     if check and st != PS_OK:
         raise PsError(st, "ps_head_rows")
     return st
@@ -466,9 +467,15 @@ def _ptr(x) -> int | None:
     raise TypeError(type(x))
 
 
+# the handle of a device's current stream without a Stream object for each call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, like: torch.Tensor | None):
     if stream is None:
         dev = like.device if like is not None else None
+        if _raw_stream is not None and dev is not None and dev.index is not None:
+            return _raw_stream(dev.index)
         return torch.cuda.current_stream(dev).cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -480,13 +487,12 @@ _NP_OF = {torch.int32: np.int32, torch.int64: np.int64, torch.float64: np.float6
 
 
 def _need(x, dtype: torch.dtype, name: str, optional: bool = False):
-    if x is None:
-        if optional:
-            return
-        raise ValueError(f"{name} is required")
     if isinstance(x, torch.Tensor):
         if x.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    elif x is None:
+        if not optional:
+            raise ValueError(f"{name} is required")
     elif isinstance(x, np.ndarray):
         if x.dtype != _NP_OF[dtype]:
             raise TypeError(f"{name} must be {_NP_OF[dtype]}, got {x.dtype}")
@@ -495,9 +501,12 @@ def _need(x, dtype: torch.dtype, name: str, optional: bool = False):
 
 
 def _row_dtype(x, name: str) -> int:
-    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be a bf16 or f32 tensor")
-    return PS_BF16 if x.dtype == torch.bfloat16 else PS_F32
+    if isinstance(x, torch.Tensor):
+        if x.dtype == torch.bfloat16:
+            return PS_BF16
+        if x.dtype == torch.float32:
+            return PS_F32
+    raise TypeError(f"{name} must be a bf16 or f32 tensor")
 
 
 def _need_rows(rules: PsLogitRules, n_rows: int) -> None:

@@ -268,8 +268,99 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
             else tok_d = map.local(tok);
         }
 
-        // What changed since the row before.  Its sequence and length have to be
-        // in order, or the patchers do not know its history.
+        const int64_t step = t - span.t0;
+        const int s = me;
+        const uint32_t lap = (uint32_t)(step / RING);
+        if (lap > 0) {
+            if (!mbar_wait_bounded(&sm.empty[s], (lap - 1) & 1u, kRuleWaitNs)) {
+                if (lane == 0) set_status(p.status, PS_DEV_TIMEOUT);
+                break;
+            }
+            done(s, r_before, slice_before);
+        }
+        r_before = r;
+        slice_before = map.slice;
+        // Logits and mask.  A mask that is not known yet is read word by word, behind
+        // the copy of all logits; the next time its size says how to copy.
+        const uint32_t bytes = (uint32_t)(map.nid * kEsz + 15) / 16 * 16;
+        const uint8_t *from = logits + src * ld_bytes;
+        const bool masked = flags & kDescMask;
+        const uint32_t *mrow = u.mask + (masked ? rm * u.mask_ld : 0);
+        const uint64_t key = (uint64_t)(rm * cut.n_slices + map.slice) + 1;
+        bool known = false;
+        if (SPARSE && masked) {
+            const uint64_t x = *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache];
+            known = x >> 16 == key;
+            if (known && (int32_t)(x & 0xffffu) * 16 * kSparseShare <= (int32_t)bytes) flags |= kDescSparse;
+        }
+        const bool sparse = flags & kDescSparse;
+        const bool copy_mask = masked && mask16 && !sparse && (known || !SPARSE);   // in bulk too
+        if (!sparse) {
+            if (lane == 0) {
+                fence_proxy_async_smem();
+                mbar_expect_tx(&sm.full[s], bytes + (copy_mask ? (map.nid + 127) / 128 * 16 : 0));
+            }
+            __syncwarp();
+            if (lane < map.n_segs) {
+                const int64_t v = ((int64_t)lane * map.n_slices + map.slice) * kSegIds;
+                bulk_g2s(sm.stage[s] + lane * (kSegIds * kEsz), from + v * kEsz,
+                         (uint32_t)min((int64_t)(kSegIds * kEsz), row_bytes - v * kEsz), &sm.full[s],
+                         policy);
+                if (copy_mask)
+                    bulk_g2s(&sm.mask[s][lane * (kSegIds / 32)], mrow + v / 32,
+                             (uint32_t)min((int64_t)(kSegIds / 8), (p.V - v + 127) / 128 * 16),
+                             &sm.full[s], policy);
+            }
+        }
+        if (masked && !copy_mask) {
+            uint32_t m[kWpl];                              // the slice's words, by lane
+            const int32_t nw = (map.nid + 31) / 32;
+#pragma unroll
+            for (int i = 0; i < kWpl; i += 4) {
+                const int at = i * 32 + lane * 4;
+                const uint32_t *word = mrow + map.global(at * 32) / 32;
+                if (mask16) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (at < nw) x = __ldg(reinterpret_cast<const uint4 *>(word));
+                    m[i] = x.x;
+                    m[i + 1] = x.y;
+                    m[i + 2] = x.z;
+                    m[i + 3] = x.w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m[i + j] = at + j < nw ? __ldg(word + j) : 0u;
+                }
+            }
+            int32_t ids = 0;
+#pragma unroll
+            for (int i = 0; i < kWpl; i += 4) {
+                reinterpret_cast<uint4 *>(sm.mask[s])[i * 8 + lane] =
+                    make_uint4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+                ids += __popc(m[i]) + __popc(m[i + 1]) + __popc(m[i + 2]) + __popc(m[i + 3]);
+            }
+            if (SPARSE && !known) {
+                ids = __reduce_add_sync(0xffffffffu, ids);
+                if (lane == 0) *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache] = key << 16 | ids;
+            }
+            if (SPARSE && sparse) {
+                fence_proxy_async_smem();
+#pragma unroll
+                for (int i = 0; i < kWpl; ++i) {
+                    const int at = ((i & ~3) * 32 + lane * 4 + (i & 3)) * 32;
+                    uint32_t x = m[i];
+                    while (x) {
+                        // the vector that holds the lowest id left
+                        const int v = (__ffs(x) - 1) / kVec * kVec;
+                        const int32_t d = at + v;
+                        if (d < map.nid)
+                            copy16(sm.stage[s] + d * kEsz, from + (int64_t)map.global(d) * kEsz);
+                        x &= ~(((1u << kVec) - 1u) << v);
+                    }
+                }
+            }
+        }
+        // In the copies' shadow: what changed since the row before.  Its sequence and
+        // length have to be in order, or the patchers do not know its history.
         const bool by_row = per_seq && !u.row_seq;
         const int64_t q = by_row ? r : (int64_t)__shfl_sync(0xffffffffu, c_seq, k);
         const int64_t q0 = by_row ? r - 1 : (int64_t)__shfl_sync(0xffffffffu, c_seq, k0);
@@ -305,100 +396,6 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
             bad |= w.bad;
         }
 
-        const int64_t step = t - span.t0;
-        const int s = me;
-        const uint32_t lap = (uint32_t)(step / RING);
-        if (lap > 0) {
-            if (!mbar_wait_bounded(&sm.empty[s], (lap - 1) & 1u, kRuleWaitNs)) {
-                if (lane == 0) set_status(p.status, PS_DEV_TIMEOUT);
-                break;
-            }
-            done(s, r_before, slice_before);
-        }
-        r_before = r;
-        slice_before = map.slice;
-        // logits and mask
-        const uint32_t bytes = (uint32_t)(map.nid * kEsz + 15) / 16 * 16;
-        const uint8_t *from = logits + src * ld_bytes;
-        const uint32_t *mrow = u.mask + (flags & kDescMask ? rm * u.mask_ld : 0);
-        bool copy_mask = false;                            // by bulk copies too
-        if (flags & kDescMask) {
-            const uint64_t key = (uint64_t)(rm * cut.n_slices + map.slice) + 1;
-            uint64_t known = 0;
-            if (SPARSE) known = *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache];
-            copy_mask = mask16 && (!SPARSE || known >> 16 == key);
-            if (SPARSE && copy_mask && (int32_t)(known & 0xffffu) * 16 * kSparseShare <= (int32_t)bytes) {
-                flags |= kDescSparse;
-                copy_mask = false;
-            }
-            if (!copy_mask) {
-                uint32_t m[kWpl];                          // the slice's words, by lane
-                const int32_t nw = (map.nid + 31) / 32;
-#pragma unroll
-                for (int i = 0; i < kWpl; i += 4) {
-                    const int at = i * 32 + lane * 4;
-                    const uint32_t *word = mrow + map.global(at * 32) / 32;
-                    if (mask16) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (at < nw) x = __ldg(reinterpret_cast<const uint4 *>(word));
-                        m[i] = x.x;
-                        m[i + 1] = x.y;
-                        m[i + 2] = x.z;
-                        m[i + 3] = x.w;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) m[i + j] = at + j < nw ? __ldg(word + j) : 0u;
-                    }
-                }
-                int32_t ids = 0;
-#pragma unroll
-                for (int i = 0; i < kWpl; i += 4) {
-                    reinterpret_cast<uint4 *>(sm.mask[s])[i * 8 + lane] =
-                        make_uint4(m[i], m[i + 1], m[i + 2], m[i + 3]);
-                    ids += __popc(m[i]) + __popc(m[i + 1]) + __popc(m[i + 2]) + __popc(m[i + 3]);
-                }
-                if constexpr (SPARSE) {
-                    ids = __reduce_add_sync(0xffffffffu, ids);
-                    if (lane == 0) *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache] = key << 16 | ids;
-                    if (ids * 16 * kSparseShare <= (int32_t)bytes) {
-                        flags |= kDescSparse;
-                        fence_proxy_async_smem();
-#pragma unroll
-                        for (int i = 0; i < kWpl; ++i) {
-                            const int at = ((i & ~3) * 32 + lane * 4 + (i & 3)) * 32;
-                            uint32_t x = m[i];
-                            while (x) {
-                                // the vector that holds the lowest id left
-                                const int v = (__ffs(x) - 1) / kVec * kVec;
-                                const int32_t d = at + v;
-                                if (d < map.nid)
-                                    copy16(sm.stage[s] + d * kEsz,
-                                           from + (int64_t)map.global(d) * kEsz);
-                                x &= ~(((1u << kVec) - 1u) << v);
-                            }
-                        }
-                    }
-                }
-            }
-        }
-        if (!(flags & kDescSparse)) {
-            const uint32_t mask_bytes = copy_mask ? (uint32_t)((map.nid + 127) / 128 * 16) : 0u;
-            if (lane == 0) {
-                fence_proxy_async_smem();
-                mbar_expect_tx(&sm.full[s], bytes + mask_bytes);
-            }
-            __syncwarp();
-            if (lane < map.n_segs) {
-                const int64_t v = ((int64_t)lane * map.n_slices + map.slice) * kSegIds;
-                bulk_g2s(sm.stage[s] + lane * (kSegIds * kEsz), from + v * kEsz,
-                         (uint32_t)min((int64_t)(kSegIds * kEsz), row_bytes - v * kEsz), &sm.full[s],
-                         policy);
-                if (copy_mask)
-                    bulk_g2s(&sm.mask[s][lane * (kSegIds / 32)], mrow + v / 32,
-                             (uint32_t)min((int64_t)(kSegIds / 8), (p.V - v + 127) / 128 * 16),
-                             &sm.full[s], policy);
-            }
-        }
         RowDesc &d = sm.desc[s];
         if (lane < n_new) d.fresh[lane] = fresh;
         if (lane == 0) {
@@ -442,7 +439,9 @@ __device__ __forceinline__ void count_token(Smem &sm, const SliceMap &map, int32
     }
     const int32_t d = map.local(id);
     if (d < 0) return;
-    atomicOr(&sm.seen[d >> 5], 1u << (d & 31));
+    // most tokens of a history have come before
+    if (!((*(volatile uint32_t *)&sm.seen[d >> 5] >> (d & 31)) & 1u))
+        atomicOr(&sm.seen[d >> 5], 1u << (d & 31));
     if (!made) return;
     uint32_t *word = reinterpret_cast<uint32_t *>(&sm.count[d & ~1]);
     const int sh = (d & 1) * 16;

@@ -463,12 +463,13 @@ __global__ void __launch_bounds__(256) score_rules_join_kernel(
     const int lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (r >= p.r.n_rows) return;
+    pdl_wait_prerequisites();                         // launched while the sums are made
     const bool bad = p.row_bad[r] != 0;
     const int n = p.cut.n_slices * kScoreParts;
     Acc a = acc_empty();
     if (!bad)
         for (int i = lane; i < n; i += 32) {
-            const float4 s = __ldg(reinterpret_cast<const float4 *>(p.parts + r * n + i));
+            const float4 s = __ldcg(reinterpret_cast<const float4 *>(p.parts + r * n + i));
             a = merge_part<NP, ENT>(a, Acc{s.x, s.y, {s.z, 0.f, 0.f}, s.w}, p.rows.g);
         }
     a = warp_merge<NP, ENT>(a, p.rows.g);
@@ -486,8 +487,16 @@ cudaError_t launch(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
         <<<(int)(tasks < sms ? tasks : sms), rule_threads<kRing>(), smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    score_rules_join_kernel<NP, ENT><<<(unsigned)((p.r.n_rows + 7) / 8), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((p.r.n_rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, score_rules_join_kernel<NP, ENT>, p);
 }
 
 template <int DT, bool ENT>
