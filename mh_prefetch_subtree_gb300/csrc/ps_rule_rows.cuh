@@ -42,7 +42,8 @@ constexpr int kFirstProducer = kSumWarps + kPatchWarps;
 template <int RING>
 constexpr int rule_threads() { return (kFirstProducer + RING) * 32; }
 constexpr int kHeld = 3;                             // of them in each lane's registers
-constexpr int kListCap = 256;                        // touched ids of a warp kept as a list
+constexpr int kListCap = 896;                        // touched ids of a warp kept as a list
+constexpr int kBiasCap = 64;                         // biased ones among them
 constexpr uint32_t kCountFull = 0xffffu;             // a count that no longer fits
 constexpr int64_t kNoSeq = INT64_MIN;
 constexpr int kMaxNew = 6;                           // new tokens of a row handed on one by one
@@ -99,7 +100,7 @@ struct RuleSmem {
     uint32_t seen[kBlocks];
     uint32_t biased[kBlocks];
     uint16_t list[kPatchWarps][kListCap];            // local numbers
-    float list_bias[kPatchWarps][kListCap];
+    float list_bias[kPatchWarps][kBiasCap];
     RowDesc desc[RING];
     RowRules rules[RING];
     uint64_t mask_ids[kMaskCache];                   // a mask and slice, and its ids there
@@ -474,15 +475,16 @@ __device__ __noinline__ const int32_t *rule_tables(Smem &sm, SliceMap map, const
     for (int i = tid; i < blocks; i += kCountThreads) sm.seen[i] = sm.biased[i] = 0;
     if (!rule_meet(sm, 3 * k + 1)) return nullptr;
     const bool fits = len - max(0, min(prompt, len)) < (int32_t)kCountFull;
-    for (int b = 0; b < len; b += kCountThreads * 4) {
-        int32_t id[4];
+    constexpr int kAhead = 8;                       // tokens that a thread asks for at once
+    for (int b = 0; b < len; b += kCountThreads * kAhead) {
+        int32_t id[kAhead];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kAhead; ++j) {
             const int i = b + j * kCountThreads + tid;
             id[j] = i < len ? __ldg(hist + i) : 0;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kAhead; ++j) {
             const int i = b + j * kCountThreads + tid;
             if (i < len) count_token(sm, map, id[j], i >= prompt, fits, bad_word);
         }
@@ -571,13 +573,14 @@ struct RuleWalk {
             const bool mine = d >= 0 && owner_of(d) == (uint32_t)wid;
             const uint32_t all = __ballot_sync(0xffffffffu, mine);
             const int32_t at = n_list + __popc(all & ((1u << lane) - 1u));
-            if (mine && at < kListCap) {
+            if (mine && at < kBiasCap) {
                 sm.list[wid][at] = (uint16_t)d;
                 sm.list_bias[wid][at] = __ldg(w.bias_values + b + lane);
             }
             n_list += __popc(all);
         }
         n_bias = n_list;
+        if (n_bias > kBiasCap) n_list = kListCap + 1;       // no list
         for (int b0 = 0; b0 < blocks; b0 += kPatchThreads) {
             const int b = b0 + lane * kPatchWarps + wid;
             uint32_t m = b < blocks ? sm.seen[b] & ~sm.biased[b] : 0u;
@@ -649,15 +652,15 @@ struct RuleWalk {
                   summand(d, i < n_bias ? sm.list_bias[wid][i] : 0.f));
             }
         } else {
+            // too many for a list: block by block, one id a lane
             int j = 0;
-            for (int b = lane * kPatchWarps + wid; b * kBlockIds < map.nid; b += kPatchThreads) {
+            for (int b = wid; b * kBlockIds < map.nid; b += kPatchWarps) {
                 const uint32_t sw = sm.seen[b], bw = sm.biased[b];
-                for (uint32_t m = sw | bw; m != 0; m &= m - 1) {
-                    const int k = __ffs(m) - 1;
-                    const uint32_t d = b * kBlockIds + k;
-                    const bool seen = (sw >> k) & 1u;
-                    const float bias = (bw >> k) & 1u ? bias_of(w.bias_ids, w.bias_values, w.n_bias,
-                                                                map.global((int32_t)d)) : 0.f;
+                if (((sw | bw) >> lane) & 1u) {
+                    const uint32_t d = b * kBlockIds + lane;
+                    const bool seen = (sw >> lane) & 1u;
+                    const float bias = (bw >> lane) & 1u ? bias_of(w.bias_ids, w.bias_values, w.n_bias,
+                                                                   map.global((int32_t)d)) : 0.f;
                     f(j++, d, seen ? inv_rho : 1.f, seen ? w.rho : 1.f, summand(d, bias));
                 }
             }
