@@ -685,7 +685,8 @@ class DeviceSubtree:
 
     Built from host arrays of the layout (chain_seg0, seg_row0, seg_cut,
     seg_src, chain_node0, acc, rej, req), the acceptance uniforms and the
-    device tensors of logits and tokens.
+    device tensors of logits and tokens.  With rules (make_rules, its row arrays
+    in the order of the scored rows) the rows are scored under them.
     """
 
     batch: PsSubtreeBatch
@@ -694,6 +695,7 @@ class DeviceSubtree:
     walk_out: PsWalkOut
     workspace: torch.Tensor
     t: dict
+    rules: PsLogitRules | None = None
 
     @classmethod
     def create(cls, *, layout, u, logits: torch.Tensor, tokens: torch.Tensor, V: int,
@@ -701,7 +703,8 @@ class DeviceSubtree:
                per_row: bool = True, sums: bool = True, path: bool = True,
                entropy: bool = False, eps: float | None = None,
                root_lp0: torch.Tensor | None = None,
-               root_lq: torch.Tensor | None = None, flags: int = 0) -> "DeviceSubtree":
+               root_lq: torch.Tensor | None = None, flags: int = 0,
+               rules: PsLogitRules | None = None) -> "DeviceSubtree":
         dev = logits.device
         i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32)).to(dev)
         t = dict(
@@ -717,6 +720,7 @@ class DeviceSubtree:
         n_seg = int(len(layout.seg_cut))
         n_chains = int(len(layout.chain_seg0)) - 1
         f64 = lambda n: torch.empty(n, dtype=torch.float64, device=dev)
+        per_row = per_row or rules is not None      # their sums are formed from these
         t["lp0"] = f64(n_rows) if per_row else None
         t["lq"] = f64(n_rows) if per_row else None
         for k in ("lp_y", "lq_y", "lp_x", "lq_x", "log_ratio"):
@@ -736,7 +740,10 @@ class DeviceSubtree:
                            logits=logits, tokens=tokens, row_index=row_index, n_rows=n_rows,
                            eps=0.01 if eps is None else eps, root_lp0=root_lp0,
                            root_lq=root_lq, flags=flags)
-        ws_bytes = ps_score_workspace_bytes(batch)
+        if rules is not None:
+            _need_rows(rules, n_rows)
+        ws_bytes = (ps_score_workspace_bytes(batch) if rules is None
+                    else ps_rules_workspace_bytes(batch))
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         sout = make_score_out(log_accept=t["log_accept"], status=t["status"], lp0=t["lp0"],
                               lq=t["lq"], lp_y=t["lp_y"], lq_y=t["lq_y"], lp_x=t["lp_x"],
@@ -746,15 +753,25 @@ class DeviceSubtree:
                          rej=t["rej"], req=t["req"], u=t["u"], max_steps=max_steps)
         wout = make_walk_out(state_seg=t["state_seg"], end_node=t["end_node"],
                              k_delta=t["k_delta"], status=t["wstatus"], path=t["path"])
-        return cls(batch=batch, tree=tree, score_out=sout, walk_out=wout, workspace=ws, t=t)
+        return cls(batch=batch, tree=tree, score_out=sout, walk_out=wout, workspace=ws, t=t,
+                   rules=rules)
 
     def score(self, stream=None) -> None:
-        ps_score_subtree(self.batch, self.score_out, self.workspace, stream)
+        if self.rules is not None:
+            self.score_rows(stream)
+            self.assemble(stream)
+        else:
+            ps_score_subtree(self.batch, self.score_out, self.workspace, stream)
 
     def score_rows(self, stream=None) -> None:
         """First half of score(): per-row log-probabilities into t['lp0'], t['lq']."""
-        ps_score_rows(self.batch, self.t["lp0"], self.t["lq"], self.t["status"],
-                      self.workspace, stream, entropy=self.t["entropy"])
+        if self.rules is not None:
+            ps_score_rows_rules(self.batch, self.rules, self.t["lp0"], self.t["lq"],
+                                self.t["status"], self.workspace, stream,
+                                entropy=self.t["entropy"])
+        else:
+            ps_score_rows(self.batch, self.t["lp0"], self.t["lq"], self.t["status"],
+                          self.workspace, stream, entropy=self.t["entropy"])
 
     def assemble(self, stream=None) -> None:
         """Second half of score(): suffix sums and log A from t['lp0'], t['lq']."""
@@ -766,8 +783,8 @@ class DeviceSubtree:
     def step(self, stream=None, fused: bool = True) -> None:
         """One pass of the whole path: score, sum and walk in one call
         (ps_score_walk_subtree), or with fused=False in two
-        (ps_score_subtree, then ps_walk_subtree)."""
-        if fused:
+        (ps_score_subtree, then ps_walk_subtree); under rules, in three."""
+        if fused and self.rules is None:
             ps_score_walk_subtree(self.batch, self.tree, self.score_out, self.walk_out,
                                   self.workspace, stream)
         else:
