@@ -86,7 +86,6 @@ ps_status ps_process_rows(const ps_logit_rules *rules, int32_t V, int32_t dtype,
     p.out = (uint8_t *)out;
     p.ld_bytes = ld * esz;
     p.out_ld_bytes = out_ld * esz;
-    p.row_bytes = ((int64_t)V * esz + 15) / 16 * 16;
     return map_cuda(launch_process_rows(p, dtype, sms, (cudaStream_t)cuda_stream));
 }
 
@@ -130,7 +129,6 @@ ps_status ps_score_rows_rules(const ps_subtree_batch *b, const ps_logit_rules *r
     q.V = b->V;
     q.dtype = b->dtype;
     q.flags = b->flags;
-    q.row_bytes = (int32_t)(((int64_t)b->V * esz + 15) / 16 * 16);
     q.npow = integer_power(b->tau);
     q.g = (float)(1.0 / b->tau);
     q.lp0 = lp0;

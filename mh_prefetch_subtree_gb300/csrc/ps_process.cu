@@ -22,7 +22,6 @@ constexpr int kRing = 3;
 
 template <int DT>
 struct ProcessSmem : RuleSmem<DT, DT == PS_BF16 ? 2 : 1, kRing> {
-    uint4 lut[kLutSize<DT>];
     int32_t row_bad[kRing];
 };
 static_assert(sizeof(ProcessSmem<PS_BF16>) <= 232448 && sizeof(ProcessSmem<PS_F32>) <= 232448,
@@ -99,24 +98,23 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) process_rows_kernel(
     constexpr uint32_t kOff = Elem<DT>::kNegInfWord;
     constexpr uint32_t kNan = DT == PS_BF16 ? 0x7fc07fc0u : 0x7fc00000u;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    fill_lut<DT>(sm.lut);
     rule_smem_init<Smem, kRing>(sm);
     __syncthreads();
 
     if (wid >= kFirstProducer) {
         rule_producer<DT, kNb, kRing, true>(
-            sm, p.r, cut, p.logits, p.ld_bytes, p.row_bytes, nullptr, p.r.n_rows, nullptr,
+            sm, p.r, cut, p.logits, p.ld_bytes, nullptr, p.r.n_rows, nullptr,
             [&](int s, int64_t r, int32_t slice) {
                 // out with the stage: whole vectors in bulk, ids after the last one by hand
                 const SliceMap map(cut, p.r.V, slice);
                 uint8_t *to = p.out + r * p.out_ld_bytes;
-                if (lane < map.n_segs) {
-                    const int64_t v = ((int64_t)lane * map.n_slices + slice) * kSegIds;
-                    const uint32_t ids = (uint32_t)min((int64_t)kSegIds, p.r.V - v);
-                    const uint32_t whole = ids / kVec * kVec;
-                    const uint8_t *from = sm.stage[s] + lane * (kSegIds * kEsz);
+                if (lane < map.pieces()) {
+                    const int32_t d = map.piece_at(lane), ids = map.piece_ids(lane);
+                    const int64_t v = map.global(d);
+                    const int32_t whole = ids / kVec * kVec;
+                    const uint8_t *from = sm.stage[s] + d * kEsz;
                     if (whole) bulk_s2g(to + v * kEsz, from, whole * kEsz);
-                    for (uint32_t i = whole; i < ids; ++i) {
+                    for (int32_t i = whole; i < ids; ++i) {
                         if constexpr (DT == PS_BF16)
                             reinterpret_cast<uint16_t *>(to)[v + i] = reinterpret_cast<const uint16_t *>(from)[i];
                         else
@@ -164,7 +162,7 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) process_rows_kernel(
                     // the lanes' vectors in an order that spreads them over the banks
                     const int k = kBv == 4 ? ((i + (lane >> 1)) & 3) : ((i + lane) & 7);
                     const uint32_t x = m >> (k * kVec);
-                    v[k] = masked_by<DT>(v[k], sm.lut, x, bad ? kNan : kOff);
+                    v[k] = masked_by<DT>(v[k], x, bad ? kNan : kOff);
                 }
             }
         }

@@ -3,10 +3,12 @@
 //
 // A block owns a slice of the vocabulary and walks down the rows, so that
 // consecutive positions of a sequence, which differ by one token of history,
-// reuse what is known about the row before.  A slice is every n-th segment of 1024
-// ids, since the ids that a history touches lie close together (common tokens have
-// low ids): with slices of neighbouring ids the blocks of the first slice took
-// 1.8 times as long as the others.  The block's warps have three jobs.  The
+// reuse what is known about the row before.  The ids that a history touches lie close
+// together (common tokens have low ids), and with slices of neighbouring ids the blocks
+// of the first slice took 1.8 times as long as the others; so the first ids are dealt
+// to the slices in segments of 1024, some for each, and only the rest is cut into runs.
+// (All in segments: 22 bulk copies for each row of a slice and as many for its mask, one
+// after another.)  The block's warps have three jobs.  The
 // producers, one a stage, take the rows in turn (one alone spent 3200 cycles on a
 // row, and a row of 48 KB has about 1900), say in a descriptor what changed since the row before,
 // and fill a ring of stages: the slice of the row's logits (bulk copies) and of its
@@ -115,58 +117,73 @@ __device__ __forceinline__ uint32_t owner_of(uint32_t d) { return (d / kBlockIds
 // A slice of the vocabulary: its ids are numbered from 0 ("local").
 struct SliceMap {
     int32_t V, n_slices, slice;
-    int32_t n_segs;             // segments of the slice
+    int32_t head;               // ids of the slice in segments
+    int32_t from;               // first id of its run
     int32_t nid;                // ids of the slice
-    float inv;
+    uint32_t inv;               // 2^32 / n_slices, rounded down
 
     __device__ SliceMap(const RuleCut &cut, int32_t V_, int32_t slice_)
-        : V(V_), n_slices(cut.n_slices), slice(slice_), inv(1.f / (float)cut.n_slices) {
-        n_segs = (cut.n_segs - slice + n_slices - 1) / n_slices;
-        const int32_t last = (n_segs - 1) * n_slices + slice;
-        nid = (n_segs - 1) * kSegIds + min(kSegIds, V - last * kSegIds);
+        : V(V_), n_slices(cut.n_slices), slice(slice_), head(cut.head * kSegIds),
+          inv(0xffffffffu / (uint32_t)cut.n_slices) {
+        from = head * n_slices + slice * cut.run;
+        nid = head + max(0, min(cut.run, V - from));
     }
-    // The local number of id v in [0, V); -1 if it is another slice's.  (The
-    // quotient of two numbers below 2^20 is off by one at most.)
+    // The local number of id v in [0, V); -1 if it is another slice's.  (A quotient
+    // below 2^20 by the reciprocal is one too small at most.)
     __device__ __forceinline__ int32_t local(int32_t v) const {
-        const int32_t j = v / kSegIds;
-        int32_t q = (int32_t)((float)j * inv);
-        int32_t rem = j - q * n_slices;
-        if (rem < 0) rem += n_slices, --q;
-        if (rem >= n_slices) rem -= n_slices, ++q;
-        return rem == slice ? q * kSegIds + v % kSegIds : -1;
+        if (v >= head * n_slices) {
+            const int32_t d = v - from;
+            return d >= 0 && d < nid - head ? head + d : -1;
+        }
+        const uint32_t j = (uint32_t)v / kSegIds;
+        uint32_t q = __umulhi(j, inv), rem = j - q * n_slices;
+        if (rem >= (uint32_t)n_slices) rem -= n_slices, ++q;
+        return rem == (uint32_t)slice ? (int32_t)(q * kSegIds + (uint32_t)v % kSegIds) : -1;
     }
     __device__ __forceinline__ int32_t global(int32_t d) const {
+        if (d >= head) return from + (d - head);
         return ((d / kSegIds) * n_slices + slice) * kSegIds + d % kSegIds;
+    }
+    // The slice is copied in pieces: segments, then the run.  Piece i begins at local
+    // id piece_at(i) and has piece_ids(i) ids.
+    __device__ __forceinline__ int pieces() const { return head / kSegIds + (nid > head); }
+    __device__ __forceinline__ int32_t piece_at(int i) const { return min(i * kSegIds, head); }
+    __device__ __forceinline__ int32_t piece_ids(int i) const {
+        return i * kSegIds < head ? kSegIds : nid - head;
     }
 };
 
-// For each byte (bfloat16) or nibble (float32) of a mask word the 32-bit masks of a
-// 16-byte vector's words.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+// A 16-byte vector with `off` in the places whose bit of `bits` (the lowest 8 or 4) is
+// 0.  A product spreads the bits over the sign bits of a word's bytes, and byte
+// permutes with sign replication make masks of them.  (A table of masks in shared
+// memory takes two instructions less a word, but its reads collide in the banks: 8000
+// rows of 151936 with masks read whole took 1060 us.)
 template <int DT>
-constexpr int kLutSize = DT == PS_BF16 ? 256 : 16;
-template <int DT>
-__device__ __forceinline__ void fill_lut(uint4 *lut) {
-    for (int i = threadIdx.x; i < kLutSize<DT>; i += blockDim.x) {
-        uint32_t k[4];
+__device__ __forceinline__ uint4 masked_by(uint4 q, uint32_t bits, uint32_t off) {
+    uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (DT == PS_BF16) {
+        // bits 0, 2, 4, 6 to 7, 15, 23, 31 (what else the sums hold reaches none of
+        // these), and 1, 3, 5, 7 likewise
+        const uint32_t even = (bits & 0x55u) * 0x02082080u, odd = (bits & 0xaau) * 0x01041040u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == PS_BF16)
-                k[j] = ((i >> (2 * j)) & 1 ? 0xffffu : 0u) | ((i >> (2 * j + 1)) & 1 ? 0xffff0000u : 0u);
-            else
-                k[j] = (i >> j) & 1 ? 0xffffffffu : 0u;
+            const uint32_t k = prmt(even, odd, 0xcc88u + j * 0x1111u);
+            w[j] = (w[j] & k) | (off & ~k);
         }
-        lut[i] = make_uint4(k[0], k[1], k[2], k[3]);
+    } else {
+        const uint32_t t = (bits & 15u) * 0x10204080u;            // bits 0 .. 3 likewise
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t k = prmt(t, t, 0x8888u + j * 0x1111u);
+            w[j] = (w[j] & k) | (off & ~k);
+        }
     }
-}
-// q with `off` in the places whose bit of `bits` is 0.
-template <int DT>
-__device__ __forceinline__ uint4 masked_by(uint4 q, const uint4 *lut, uint32_t bits, uint32_t off) {
-    const uint4 k = lut[bits & (kLutSize<DT> - 1)];
-    q.x = (q.x & k.x) | (off & ~k.x);
-    q.y = (q.y & k.y) | (off & ~k.y);
-    q.z = (q.z & k.z) | (off & ~k.z);
-    q.w = (q.w & k.w) | (off & ~k.w);
-    return q;
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The block h of 32 ids that a lane of a warp that works on all ids takes.
@@ -210,14 +227,13 @@ struct RuleSpan {
 template <int DT, int NB, int RING, bool SPARSE, typename Done>
 __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const RulesParams &p,
                                               const RuleCut &cut, const uint8_t *logits,
-                                              int64_t ld_bytes, int64_t row_bytes,
+                                              int64_t ld_bytes,
                                               const int64_t *row_index, int64_t n_logit_rows,
                                               const int32_t *tokens, Done done) {
     using Smem = RuleSmem<DT, NB, RING>;
     constexpr int kEsz = Smem::kEsz;
     constexpr int kWpl = Smem::kBlocks / 32;               // mask words of a lane
     constexpr int kVec = 16 / kEsz;                        // ids of a vector
-    static_assert(Smem::kIds / kSegIds <= 32, "a lane copies a segment");
     const ps_logit_rules &u = p.rules;
     const int lane = threadIdx.x & 31, me = (threadIdx.x >> 5) - kFirstProducer;
     const RuleSpan span(p.n_rows, cut.n_slices);
@@ -302,14 +318,12 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
                 mbar_expect_tx(&sm.full[s], bytes + (copy_mask ? (map.nid + 127) / 128 * 16 : 0));
             }
             __syncwarp();
-            if (lane < map.n_segs) {
-                const int64_t v = ((int64_t)lane * map.n_slices + map.slice) * kSegIds;
-                bulk_g2s(sm.stage[s] + lane * (kSegIds * kEsz), from + v * kEsz,
-                         (uint32_t)min((int64_t)(kSegIds * kEsz), row_bytes - v * kEsz), &sm.full[s],
-                         policy);
+            if (lane < map.pieces()) {
+                const int32_t d = map.piece_at(lane), ids = map.piece_ids(lane), v = map.global(d);
+                bulk_g2s(sm.stage[s] + d * kEsz, from + (int64_t)v * kEsz,
+                         (uint32_t)(ids * kEsz + 15) / 16 * 16, &sm.full[s], policy);
                 if (copy_mask)
-                    bulk_g2s(&sm.mask[s][lane * (kSegIds / 32)], mrow + v / 32,
-                             (uint32_t)min((int64_t)(kSegIds / 8), (p.V - v + 127) / 128 * 16),
+                    bulk_g2s(&sm.mask[s][d / 32], mrow + v / 32, (uint32_t)(ids + 127) / 128 * 16,
                              &sm.full[s], policy);
             }
         }

@@ -19,15 +19,16 @@ struct ProcessParams {
     uint8_t *out;               // may be logits itself
     int64_t ld_bytes;
     int64_t out_ld_bytes;
-    int64_t row_bytes;          // of the V logits, rounded up to 16
 };
 
-// How the vocabulary is cut for the kernels that stream rows: into segments of
-// kSegIds ids, dealt to the slices in turn.
+// How the vocabulary is cut for the kernels that stream rows.  A slice has `head`
+// segments of kSegIds ids, which are dealt to the slices in turn from the first id on,
+// and a run of the ids after those.
 constexpr int32_t kSegIds = 1024;
 struct RuleCut {
-    int32_t n_segs;
     int32_t n_slices;
+    int32_t head;               // segments of a slice
+    int32_t run;                // ids of a run, a multiple of 128
 };
 // most: ids of a slice at most (a multiple of kSegIds).
 RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows);

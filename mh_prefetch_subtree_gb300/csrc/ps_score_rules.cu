@@ -33,7 +33,6 @@ constexpr float kLeast = 8.673617379884035e-19f;     // 2^-60
 
 template <int DT>
 struct ScoreSmem : RuleSmem<DT, DT == PS_BF16 ? 2 : 1, kRing> {
-    uint4 lut[kLutSize<DT>];                         // mask bits -> which words stay
     uint4 off[8];                                    // a block that does not count
     // processed logits of the first touched ids of each patcher, and how many
     float touched[kRing][kPatchWarps][kTouched];
@@ -104,7 +103,7 @@ struct LaneIds {
 // of a.  A rolled loop: the eight vectors in one run of code would not fit the
 // instruction caches that three kinds of warps share.
 template <int DT, bool MASKED, typename F>
-__device__ __forceinline__ void each_pair(const LaneIds &l, const uint4 *lut, uint32_t off, F f) {
+__device__ __forceinline__ void each_pair(const LaneIds &l, uint32_t off, F f) {
     constexpr int kBits = DT == PS_BF16 ? 8 : 4;
     int k = l.first;
     uint4 qa = l.a[k], qb = l.b[k];
@@ -114,8 +113,8 @@ __device__ __forceinline__ void each_pair(const LaneIds &l, const uint4 *lut, ui
         k = (k + 1) & 3;
         const uint4 na = l.a[k], nb = l.b[k];            // the next ones
         if constexpr (MASKED) {
-            qa = masked_by<DT>(qa, lut, ma, off);
-            qb = masked_by<DT>(qb, lut, mb, off);
+            qa = masked_by<DT>(qa, ma, off);
+            qb = masked_by<DT>(qb, mb, off);
             ma >>= kBits;
             mb >>= kBits;
         }
@@ -126,10 +125,10 @@ __device__ __forceinline__ void each_pair(const LaneIds &l, const uint4 *lut, ui
 }
 
 template <int DT, bool MASKED>
-__device__ __forceinline__ float max_of(const LaneIds &l, const uint4 *lut, uint32_t off) {
+__device__ __forceinline__ float max_of(const LaneIds &l, uint32_t off) {
     if constexpr (DT == PS_BF16) {
         uint32_t m = 0xff80ff80u;
-        each_pair<DT, MASKED>(l, lut, off, [&](uint4 a, uint4 b) {
+        each_pair<DT, MASKED>(l, off, [&](uint4 a, uint4 b) {
             a.x = max_nan_bf16x2(max_nan_bf16x2(a.x, a.y), max_nan_bf16x2(a.z, a.w));
             b.x = max_nan_bf16x2(max_nan_bf16x2(b.x, b.y), max_nan_bf16x2(b.z, b.w));
             m = max_nan_bf16x2(m, max_nan_bf16x2(a.x, b.x));
@@ -137,7 +136,7 @@ __device__ __forceinline__ float max_of(const LaneIds &l, const uint4 *lut, uint
         return max_nan_f32(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     } else {
         float m = -INFINITY;
-        each_pair<DT, MASKED>(l, lut, off, [&](uint4 a, uint4 b) {
+        each_pair<DT, MASKED>(l, off, [&](uint4 a, uint4 b) {
             const auto top = [](uint4 q) {
                 return max_nan_f32(max_nan_f32(__uint_as_float(q.x), __uint_as_float(q.y)),
                                    max_nan_f32(__uint_as_float(q.z), __uint_as_float(q.w)));
@@ -157,7 +156,7 @@ __device__ __forceinline__ uint32_t raised(uint32_t w) {
 
 // The lane's sums.
 template <int DT, int NP, bool ENT, bool MASKED>
-__device__ __forceinline__ Sums sum_dense(const LaneIds &l, const uint4 *lut, uint32_t off, float ref,
+__device__ __forceinline__ Sums sum_dense(const LaneIds &l, uint32_t off, float ref,
                                           float g, bool raise) {
     constexpr int kPairs = DT == PS_BF16 ? 4 : 2;
     const float2 L2 = make_float2(kLog2e, kLog2e), nR2 = make_float2(-ref, -ref);
@@ -165,7 +164,7 @@ __device__ __forceinline__ Sums sum_dense(const LaneIds &l, const uint4 *lut, ui
     float2 a1[4], at[4], ay[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) a1[j] = at[j] = ay[j] = make_float2(0.f, 0.f);
-    each_pair<DT, MASKED>(l, lut, off, [&](uint4 qa, uint4 qb) {
+    each_pair<DT, MASKED>(l, off, [&](uint4 qa, uint4 qb) {
         if (ENT && raise) {
             qa = make_uint4(raised<DT>(qa.x), raised<DT>(qa.y), raised<DT>(qa.z), raised<DT>(qa.w));
             qb = make_uint4(raised<DT>(qb.x), raised<DT>(qb.y), raised<DT>(qb.z), raised<DT>(qb.w));
@@ -310,14 +309,13 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const float g = p.rows.g;
 
-    fill_lut<DT>(sm.lut);
     if (threadIdx.x < kBv) sm.off[threadIdx.x] = make_uint4(kOff, kOff, kOff, kOff);
     rule_smem_init<Smem, kRing>(sm);
     __syncthreads();
 
     if (wid >= kFirstProducer) {
         rule_producer<DT, kNb, kRing, true>(sm, p.r, p.cut, p.rows.logits, p.rows.ld_bytes,
-                                            p.rows.row_bytes, p.rows.row_index, p.rows.n_logit_rows,
+                                            p.rows.row_index, p.rows.n_logit_rows,
                                             p.rows.tokens, [](int, int64_t, int32_t) {});
         return;
     }
@@ -425,7 +423,7 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
             // and -inf raised (among the logits it makes 2^y y NaN)
             for (int look = ENT;; ++look) {
                 if (look == 1) {
-                    float x = masked ? max_of<DT, true>(l, sm.lut, kOff) : max_of<DT, false>(l, sm.lut, kOff);
+                    float x = masked ? max_of<DT, true>(l, kOff) : max_of<DT, false>(l, kOff);
                     if (x <= kAbsentBelow) x = -INFINITY;
                     x = warp_max_nan(max_nan_f32(x, px));
                     if (x == -INFINITY) {             // nothing here
@@ -434,8 +432,8 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
                     }
                     ref = x * kLog2e;
                 }
-                join_lanes(masked ? sum_dense<DT, NP, ENT, true>(l, sm.lut, kOff, ref, g, look == 2)
-                                  : sum_dense<DT, NP, ENT, false>(l, sm.lut, kOff, ref, g, look == 2));
+                join_lanes(masked ? sum_dense<DT, NP, ENT, true>(l, kOff, ref, g, look == 2)
+                                  : sum_dense<DT, NP, ENT, false>(l, kOff, ref, g, look == 2));
                 if (ENT ? look == 2 || sum.y1 == sum.y1 || sum.s1 != sum.s1 : look || in_range()) break;
             }
         }
@@ -513,16 +511,27 @@ cudaError_t launch_np(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
 }  // namespace
 
 // As few slices as hold the vocabulary, or where there are few rows as many as
-// give every SM a block (of a segment at least).
+// give every SM a block (of 1024 ids at least).  Segments of a slice (8000 rows of 151936
+// bf16 without masks, 150 rows of 50021 float32 with long histories): none 764 and 109 us,
+// 2: 626 and 78, 9: 599 and 68, all: 611 and 65, but with masks, whose segments are
+// copied too, 9: 765 and all: 800.
 RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows) {
-    constexpr int64_t kBlocks = 152;
-    RuleCut c;
-    c.n_segs = (int32_t)(((int64_t)V + kSegIds - 1) / kSegIds);
-    const int64_t per = most / kSegIds, least = (c.n_segs + per - 1) / per;
-    int64_t slices = kBlocks / (n_rows > 0 ? n_rows : 1);
-    if (slices > c.n_segs) slices = c.n_segs;
-    c.n_slices = (int32_t)(slices > least ? slices : least);
-    return c;
+    constexpr int64_t kBlocks = 152, kHead = 9;
+    int64_t n = kBlocks / (n_rows > 0 ? n_rows : 1);
+    if (n > V / 1024) n = V / 1024;
+    if (n < 1) n = 1;
+    for (;; ++n) {
+        RuleCut c;
+        const int64_t head = V > kSegIds ? (V / kSegIds - 1) / n : 0;
+        c.head = (int32_t)(head < kHead ? head : kHead);
+        const int64_t rest = V - n * c.head * kSegIds;           // > 0
+        const int64_t run = ((rest + n - 1) / n + 127) / 128 * 128;
+        if (c.head * kSegIds + run > most) continue;
+        c.run = (int32_t)run;
+        // without segments the last slices may hold nothing
+        c.n_slices = (int32_t)(c.head ? n : (rest + run - 1) / run);
+        return c;
+    }
 }
 
 RuleCut score_cut(int32_t V, int32_t dtype, int64_t n_rows) {
