@@ -58,6 +58,8 @@ SHAPES = [  # rows, V, K, group
     (1, 1, 32, 32), (1, 17, 64, 64), (3, 100, 128, 128), (8, 1000, 96, 32), (9, 333, 192, 64),
     (16, 515, 256, 256), (1, 4097, 1024, 128), (5, 2050, 2080, 32), (17, 1040, 512, 64),
     (33, 777, 640, 128), (64, 1500, 1024, 32), (65, 300, 384, 128), (130, 129, 256, 64),
+    # long rows of hidden states, 17 rows and more
+    (40, 515, 2048, 128), (64, 1111, 4096, 128), (50, 200, 4608, 64), (100, 130, 4096, 512),
 ]
 
 
