@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libps.so")
 SOURCES = ["ps_score_rows.cu", "ps_assemble.cu", "ps_walk.cu", "ps_carry.cu", "ps_tree.cu", "ps_selftest.cu",
-           "ps_api.cu", "ps_process.cu", "ps_score_rules.cu", "ps_head.cu", "ps_api_rules.cu"]
+           "ps_api.cu", "ps_process.cu", "ps_score_rules.cu", "ps_head.cu", "ps_head_tile.cu", "ps_api_rules.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                  "-I", os.path.join(ROOT, "include")]

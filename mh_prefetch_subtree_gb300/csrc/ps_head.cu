@@ -1,4 +1,5 @@
-// Logits rows from hidden states and a 4-bit output head (ps_head_rows).
+// Logits rows from hidden states and a 4-bit output head (ps_head_rows): few hidden
+// rows, or sizes that ps_head_tile.cu does not take.
 //
 // For few rows the weights are all that moves: V K / 2 bytes, each read once.
 // A warp takes 16 MT vocabulary rows and multiplies them by 8 NT hidden rows with
@@ -26,9 +27,6 @@
 // What bounds it: 8 weights take 9 instructions to unpack, 5 of them on the integer
 // pipe, which takes one every other cycle; a multiprocessor gets 1 KB of weights
 // every 43 cycles from memory.
-#include <cuda_fp16.h>
-#include <cuda_bf16.h>
-
 #include "ps_head.cuh"
 
 namespace ps {
@@ -44,20 +42,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
-__device__ __forceinline__ __half2 h2_of(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
-
-// The four pairs (j, j + 4) of a word less the zero, as float16.  z1 holds
-// -(1024 + zero) twice, z16 -(64 + zero).
-__device__ __forceinline__ void unpack(uint32_t word, uint32_t z1, uint32_t z16, uint32_t (&x)[4]) {
-    const uint32_t w8 = word >> 8;
-    const __half2 sixteenth = h2_of(0x2c002c00u);
-    x[0] = h2_bits(__hadd2(h2_of((word & 0x000f000fu) | 0x64006400u), h2_of(z1)));
-    x[1] = h2_bits(__hfma2(h2_of((word & 0x00f000f0u) | 0x64006400u), sixteenth, h2_of(z16)));
-    x[2] = h2_bits(__hadd2(h2_of((w8 & 0x000f000fu) | 0x64006400u), h2_of(z1)));
-    x[3] = h2_bits(__hfma2(h2_of((w8 & 0x00f000f0u) | 0x64006400u), sixteenth, h2_of(z16)));
 }
 
 // The words of a quad's 128 k, 4 in each lane, regrouped so that each unit of U k
@@ -135,12 +119,6 @@ struct ScaleZero<float> {
     __device__ __forceinline__ uint32_t zero() const { return z; }
 };
 
-// x 2^e, where 2^e alone may be out of range.
-__device__ __forceinline__ float times_power(float x, int e) {
-    const int a = e / 2, b = e - a;
-    return x * __int_as_float((a + 127) << 23) * __int_as_float((b + 127) << 23);
-}
-
 // U: elements of k whose sums share a scale (32, 64 or 128).  wk warps of a block
 // share a tile's k.  K is laid out whole, or where it does not fit (then NT is 1)
 // in parts that all warps of the block work on together.
@@ -188,21 +166,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) head_rows_kernel(const HeadPara
             // the power of two of each hidden row, from its largest finite element
             __syncthreads();
             for (int n = wid; n < kCols; n += kHeadWarps) {
-                uint32_t top = 0;
-                if (n0 + n < p.n_rows)
-                    for (int i = lane; i < K / 8; i += 32) {
-                        const uint4 h = __ldg(reinterpret_cast<const uint4 *>(
-                                                  p.hidden + (int64_t)(n0 + n) * p.hidden_ld) + i);
-                        const uint32_t x[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t lo = x[j] & 0x7fffu, hi = x[j] >> 16 & 0x7fffu;
-                            if (lo < 0x7f80u) top = max(top, lo);
-                            if (hi < 0x7f80u) top = max(top, hi);
-                        }
-                    }
-                top = __reduce_max_sync(0xffffffffu, top);
-                if (lane == 0) power[n] = top ? 14 + 127 - max(1, (int)(top >> 7)) : 0;
+                const int e = n0 + n < p.n_rows
+                                  ? row_power(p.hidden + (int64_t)(n0 + n) * p.hidden_ld, K, lane) : 0;
+                if (lane == 0) power[n] = e;
             }
             __syncthreads();
         }
@@ -233,15 +199,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) head_rows_kernel(const HeadPara
                         tg = in / W;
                         at = u * W + in % W;
                     }
-                    // pairs (0, 4), (1, 5), (2, 6), (3, 7)
-                    const int e = power[n];
-                    auto pair = [&](uint32_t lo, uint32_t hi) {
-                        return h2_bits(__floats2half2_rn(times_power(__uint_as_float(lo), e),
-                                                         times_power(__uint_as_float(hi), e)));
-                    };
-                    smem4[(size_t)(n / 8) * kn + at * 32 + (n % 8) * 4 + tg] =
-                        make_uint4(pair(h.x << 16, h.z << 16), pair(h.x & 0xffff0000u, h.z & 0xffff0000u),
-                                   pair(h.y << 16, h.w << 16), pair(h.y & 0xffff0000u, h.w & 0xffff0000u));
+                    smem4[(size_t)(n / 8) * kn + at * 32 + (n % 8) * 4 + tg] = hidden_pairs(h, make_float2(times_power(1.f, power[n] / 2), times_power(1.f, power[n] - power[n] / 2)));
                 }
                 __syncthreads();
             }
@@ -459,9 +417,9 @@ cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
 }
 
 // Hidden rows of a block: 8, 16 or 32, as many as there are and as fit.  With 8, a
-// warp takes 32 vocabulary rows (1 row of 151936 x 4096: 74 us, with 16: 96); with more
-// there are not the registers (16 rows: 105 us with 32, 98 with 16).  12 warps instead of
-// 16 pay with 32 hidden rows only (64 rows of 262144 x 2048: 254 and 279 us).
+// warp takes 32 vocabulary rows (1 row of 151936 x 4096: 68 us, with 16: 96); with more
+// there are not the registers (16 rows: 105 us with 32, 92 with 16).  12 warps instead of
+// 16 pay with 32 hidden rows only (64 rows of 262144 x 2048: 254 and 279 us; 8 warps 274).
 template <int U, typename ScaleT>
 cudaError_t launch_n(const HeadParams &p, int sms, cudaStream_t stream) {
     const int64_t fits = kHeadSmem / ((int64_t)p.head.K * 16);
@@ -479,6 +437,7 @@ cudaError_t launch_u(const HeadParams &p, int sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_head_rows(const HeadParams &p, int sms, cudaStream_t stream) {
+    if (head_tile_takes(p, sms)) return launch_head_tile(p, sms, stream);
     if (p.head.group == 32) return launch_u<32>(p, sms, stream);
     if (p.head.group == 64) return launch_u<64>(p, sms, stream);
     return launch_u<128>(p, sms, stream);

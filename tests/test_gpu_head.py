@@ -127,6 +127,49 @@ def test_same_bits_again_and_on_another_stream():
         assert torch.equal(run(h[p].contiguous(), q, s, z, 128, torch.float32), a[p])
 
 
+# heads large enough for the tensor memory kernel: one block's hidden rows and two
+# blocks', 32 and 64 at a time, several times, parts of a copy and of a tile left over
+LARGE = [(17, 40000, 256, 64), (33, 40009, 288, 32), (32, 41111, 640, 128), (64, 39999, 1024, 512),
+         (130, 39000, 320, 64), (64, 39425, 1120, 32), (50, 40321, 1216, 64), (20, 40000, 2304, 256),
+         (70, 39900, 2112, 64)]
+
+
+@pytest.mark.parametrize("n,V,K,group", LARGE)
+@pytest.mark.parametrize("scale,zeros,dtype", [
+    (torch.bfloat16, True, torch.float32), (torch.float32, False, torch.bfloat16)])
+def test_large_heads(n, V, K, group, scale, zeros, dtype):
+    h, q, s, z = case(n, V, K, group, scale, zeros, seed=n + V, hidden_ld=K + 8)
+    check(run(h, q, s, z, group, dtype), h, q, s, z, group)
+
+
+@pytest.mark.parametrize("n,K", [(40, 512), (40, 1280)])
+def test_large_heads_keep_rows_apart(n, K):
+    """Extremes, a NaN and an infinity of one row stay there; the same bits again,
+    for rows in another order, and on another stream."""
+    V = 39300
+    h, q, s, z = case(n, V, K, 64, torch.float32, True, seed=9)
+    q[:64], q[64:128] = 0, 255
+    z[:32], z[32:64] = 0, 15
+    s[3], s[4] = 0.0, -s[4]
+    h[2] *= 2.0 ** 100
+    h[3] *= 2.0 ** -100
+    h[4] = 0
+    want = run(h, q, s, z, 64, torch.float32)
+    check(want, h, q, s, z, 64)
+    assert (want[4] == 0).all()
+    p = torch.randperm(n, generator=torch.Generator().manual_seed(1))
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        assert torch.equal(run(h[p].contiguous(), q, s, z, 64, torch.float32, stream=st), want[p])
+    h[1, 5], s[50, 1], h[7, K - 1] = float("nan"), float("inf"), float("-inf")
+    got = run(h, q, s, z, 64, torch.float32)
+    assert torch.isnan(got[1]).all() and not torch.isfinite(got[7]).any()
+    rest = [i for i in range(n) if i not in (1, 7)]
+    cols = [i for i in range(V) if i != 50]
+    assert torch.equal(got[rest][:, cols], want[rest][:, cols])
+    assert not torch.isfinite(got[rest][:, 50]).any()
+
+
 def test_no_rows():
     h, q, s, z = case(0, 40, 32, 32, torch.float32, False)
     assert run(h, q, s, z, 32, torch.float32).shape == (0, 40)
