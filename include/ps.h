@@ -594,8 +594,12 @@ ps_status ps_score_rows_rules(const ps_subtree_batch *batch, const ps_logit_rule
  * An output head with 4-bit weights and group scales: it makes the logits rows
  * while proposals are decoded, one row for each sequence that decodes.
  *     logits[r][v] = sum_k hidden[r][k] * scale[v][k / group] * (q[v][k] - zero[v][k / group])
- * q - zero is exact, products and sums are float32, scales are applied to each
- * group's (or each 128 elements') sum; a bfloat16 result is rounded once.
+ * q - zero is exact.  A hidden row is scaled by a power of two into the range of
+ * float16, which is exact but for elements below 2^-29 of the row's largest, which
+ * are rounded to about 2^-39 of it.  Products are then exact and sums float32;
+ * scales are applied to each group's (or each 128 elements') sum; a bfloat16
+ * result is rounded once.  The order of the sums depends on the sizes, not on the
+ * values: the same call gives the same bits.
  *
  * V, K         vocabulary and hidden size; K is a multiple of group.
  * group        32, 64, or a multiple of 128.
@@ -621,7 +625,8 @@ typedef struct {
  *         multiple of 8, >= K).
  * logits  [n_rows][ld] of dtype (PS_BF16 or PS_F32), rows as in
  *         ps_subtree_batch; elements V..ld-1 of a row are not written.
- * n_rows == 0 does nothing.
+ * n_rows == 0 does nothing.  The kernels' waits on copies and products are
+ * bounded; if one ever ran out, the logits not yet made would be NaN.
  */
 ps_status ps_head_rows(const ps_head *head, const void *hidden, int64_t hidden_ld, int32_t n_rows,
                        void *logits, int64_t ld, int32_t dtype, void *cuda_stream);

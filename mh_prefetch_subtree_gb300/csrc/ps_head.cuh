@@ -44,7 +44,7 @@ __device__ __forceinline__ float times_power(float x, int e) {
 // found by one warp; 0 for a row of zeros.
 __device__ __forceinline__ int row_power(const uint16_t *row, int32_t K, int lane) {
     uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = lane; i < K / 8; i += 32) {
         const uint4 h = __ldg(reinterpret_cast<const uint4 *>(row) + i);
         const uint32_t x[4] = {h.x, h.y, h.z, h.w};

@@ -16,7 +16,7 @@
 // second operand.  Where N rows of K do not fit there, two blocks of a cluster hold
 // half of the rows each and one thread issues the products of both: 256 vocabulary
 // rows, 128 in each block's tensor memory.  (Dividing K instead, each block's sums
-// going to the other at the end of a tile, took 227 us where this takes 194; mma.sync
+// going to the other at the end of a tile, took 227 us where this takes 188; mma.sync
 // with weights unpacked once for each 32 hidden rows 254: 64 rows of 262144 x 2048,
 // group 64, where the weights alone need 47 us.)
 //
@@ -24,9 +24,11 @@
 //
 // What bounds it: the round of a unit.  A unit goes through three hand-overs, two of
 // them between blocks where there is a cluster, and tensor memory holds two or three
-// units' sums.  64 rows of 262144 x 2048: 150 us with groups of 128, 194 with 64, 326
-// with 32; without unpacking 132, 184, 323.  The tensor pipe is active about an eighth
-// of the time.
+// units' sums; the warps that take sums in are at work two thirds of the time, about
+// 1000 cycles a unit.  64 rows of 262144 x 2048: 145 us with groups of 128, 188 with
+// 64, 324 with 32; without unpacking 132, 184, 323.  The tensor pipe is active 16% of
+// the time with groups of 64, the issue slots 54%.  (16 rows at a time took 116 us for
+// 151936 x 4096 where ps_head.cu takes 92.)
 //
 // Every wait is bounded; where one runs out, the block goes on without waiting and
 // stores NaN for what it could not make.
@@ -70,6 +72,13 @@ __device__ __forceinline__ void arrive_at(uint64_t *bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
         "mbarrier.arrive.release.cta.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_addr(bar)), "r"(rank)
+        : "memory");
+}
+// The same variable of the cluster's block `rank`.
+__device__ __forceinline__ void store_at(float2 *to, uint32_t rank, float x, float y) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+        "st.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(smem_addr(to)), "r"(rank), "f"(x), "f"(y)
         : "memory");
 }
 __device__ __forceinline__ void arrive(uint64_t *bar) {
@@ -298,24 +307,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     Place copy{unpacks ? (uint32_t)wid / 4 : 0u, 0}, weights{0, 0}, sums{0, 0};
     for (int col = id % member; col < n_cols; col += member) {
         const int n0 = col * N;
-        if (wid < 8 * kPipes) {
-            for (int n = wid; n < N; n += 8 * kPipes) {
-                const int e = n0 + n < p.n_rows
-                                  ? row_power(p.hidden + (int64_t)(n0 + n) * p.hidden_ld, K, lane) : 0;
-                if (lane == 0) {
-                    scale_back[n] = make_float2(times_power(1.f, -(e / 2)), times_power(1.f, e / 2 - e));
-                    if (n / kHere == rank)
-                        scale_to[n % kHere] = make_float2(times_power(1.f, e / 2), times_power(1.f, e - e / 2));
-                }
-            }
+        // the powers of two of this block's rows; a cluster's blocks tell each other theirs
+        for (int n = wid; n < kHere; n += kTileWarps) {
+            const int row = n0 + rank * kHere + n;
+            const int e = row < p.n_rows ? row_power(p.hidden + (int64_t)row * p.hidden_ld, K, lane) : 0;
+            if (lane == 0) scale_to[n] = make_float2(times_power(1.f, e / 2), times_power(1.f, e - e / 2));
+            if (lane < C)
+                store_at(&scale_back[rank * kHere + n], lane, times_power(1.f, -(e / 2)), times_power(1.f, e / 2 - e));
         }
         __syncthreads();
+        // 8 rows of 4 times 8 k a warp: whole sectors read, no bank written twice
 #pragma unroll 4
         for (int i = threadIdx.x; i < K / 8 * kHere; i += kTileThreads) {
-            const int n = i % kHere, row = n0 + rank * kHere + n;
+            const int n = i / 32 % (kHere / 8) * 8 + i % 8, c = i / (4 * kHere) * 4 + i / 8 % 4;
+            const int row = n0 + rank * kHere + n;
             uint4 h = make_uint4(0, 0, 0, 0);
-            if (row < p.n_rows) h = __ldg(reinterpret_cast<const uint4 *>(p.hidden + (int64_t)row * p.hidden_ld) + i / kHere);
-            hid[i] = hidden_pairs(h, scale_to[n]);
+            if (row < p.n_rows) h = __ldg(reinterpret_cast<const uint4 *>(p.hidden + (int64_t)row * p.hidden_ld) + c);
+            hid[c * kHere + n] = hidden_pairs(h, scale_to[n]);
         }
         asm volatile("fence.proxy.async;" ::: "memory");
         sync_all<C>();
@@ -407,12 +415,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         z[0] = __funnelshift_r(z[0], z[1], 8);
                         z[1] >>= 8;
                         const uint32_t z1 = zero * 0x10001u + 0xe400e400u, z16 = zero * 0x100010u + 0xd400d400u;
+                        uint4 q[U / 32];
+#pragma unroll
+                        for (int c = 0; c < U / 32; ++c)
+                            q[c] = *reinterpret_cast<const uint4 *>(
+                                ring + at * kRingBytes + row * kStepBytes +
+                                ((i % kUnitsStep * (U / 32) + c) ^ (row & 7)) * 16);
 #pragma unroll
                         for (int c = 0; c < U / 32; ++c) {
-                            const int piece = i % kUnitsStep * (U / 32) + c;
-                            const uint4 q = *reinterpret_cast<const uint4 *>(
-                                ring + at * kRingBytes + row * kStepBytes + (piece ^ (row & 7)) * 16);
-                            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                            const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
                             uint32_t x[16];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
@@ -489,13 +500,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 tmem_loaded(x[c]);
-                                if (h == N / 32 - 1 && c == 1) {
-                                tc_before();
-                                __syncwarp();
-                                if (lane == 0) {
-                                    if (C == 1) arrive(&bars.taken[pipe][slot]);
-                                    else arrive_at(&bars.taken[pipe][slot], 0);
-                                }
+                                if (h == N / 32 - 1 && c == 1) {      // all are in registers
+                                    tc_before();
+                                    __syncwarp();
+                                    if (lane == 0) {
+                                        if (C == 1) arrive(&bars.taken[pipe][slot]);
+                                        else arrive_at(&bars.taken[pipe][slot], 0);
+                                    }
                                 }
 #pragma unroll
                                 for (int j = 0; j < 8; ++j)
@@ -527,7 +538,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int n = 0; n < N; ++n) store(n, sum[n]);
             }
         }
-        __syncthreads();
+        sync_all<C>();
     }
     // The sums of all products have been taken in, so nothing is in flight; after a
     // wait that ran out, copies and products may be, and are waited for.
