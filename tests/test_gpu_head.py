@@ -170,6 +170,17 @@ def test_large_heads_keep_rows_apart(n, K):
     assert not torch.isfinite(got[rest][:, 50]).any()
 
 
+def test_more_groups_of_rows_than_blocks():
+    """Each block takes several groups of hidden rows, one after another."""
+    n, V, K, group = 5003, 39001, 1056, 32
+    h, q, s, z = case(n, V, K, group, torch.bfloat16, True, seed=10)
+    out = torch.empty((n, 39008), dtype=torch.bfloat16, device=DEV)
+    head = ps.make_head(q=q.to(DEV), scales=s.to(DEV), zeros=z.to(DEV), group=group)
+    ps.ps_head_rows(head, h.to(DEV), out)
+    rows = [0, 31, 63, 64, 2500, 4863, 4864, 4900, 4991, 4992, 5002]
+    check(out[rows].cpu()[:, :V], h[rows], q, s, z, group)
+
+
 def test_no_rows():
     h, q, s, z = case(0, 40, 32, 32, torch.float32, False)
     assert run(h, q, s, z, 32, torch.float32).shape == (0, 40)
