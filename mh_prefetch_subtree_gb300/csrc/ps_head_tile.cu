@@ -602,7 +602,7 @@ template <int U, int N, int C, typename ScaleT>
 cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     const int K = p.head.K, fixed = N / C * 2 * K;
     // static shared memory and the alignment of the ring take less than 3 KB
-    int n_ring = (kSmemB - 3072 - fixed) / kRingBytes;
+    int n_ring = (kSmemB - 3 * 1024 - fixed) / kRingBytes;
     if (n_ring > kMostRing) n_ring = kMostRing;
     const int smem = 1024 + fixed + n_ring * kRingBytes;
 
