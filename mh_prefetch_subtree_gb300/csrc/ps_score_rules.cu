@@ -455,6 +455,13 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
     }
 }
 
+// Empties a part whose exponentials are 0 next to those of reference M, under tau as well.
+// (A part of logits like -1e12 has sums of no meaning: a product's rounding is 2^16 there,
+// so they may be infinite, and infinity times 0 would be NaN.)  Keeps NaN.
+__device__ __forceinline__ void drop_far(Acc &a, float M, float far) {
+    if (a.R < M - far) a = acc_empty();
+}
+
 // One warp a row: its partial sums joined in their order, then the results.
 template <int NP, bool ENT>
 __global__ void __launch_bounds__(256) score_rules_join_kernel(
@@ -465,14 +472,23 @@ __global__ void __launch_bounds__(256) score_rules_join_kernel(
     pdl_wait_prerequisites();                         // launched while the sums are made
     const bool bad = p.row_bad[r] != 0;
     const int n = p.cut.n_slices * kScoreParts;
+    const float far = 2048.f / fminf(p.rows.g, 1.f);
     Acc a = acc_empty();
     if (!bad)
         for (int i = lane; i < n; i += 32) {
             const float4 s = __ldcg(reinterpret_cast<const float4 *>(p.parts + r * n + i));
-            a = merge_part<NP, ENT>(a, Acc{s.x, s.y, {s.z, 0.f, 0.f}, s.w}, p.rows.g);
+            Acc b{s.x, s.y, {s.z, 0.f, 0.f}, s.w};
+            drop_far(a, b.R, far);
+            drop_far(b, a.R, far);
+            a = merge_part<NP, ENT>(a, b, p.rows.g);
         }
+    const float tok = bad ? 0.f : p.tok_logit[r];
+    float top = fmaxf(a.R, tok * kLog2e);             // the sums leave the token out
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    drop_far(a, top, far);
     a = warp_merge<NP, ENT>(a, p.rows.g);
-    if (lane == 0) finalize_row<NP, ENT>(p.rows, r, a, bad ? 0.f : p.tok_logit[r], bad);
+    if (lane == 0) finalize_row<NP, ENT>(p.rows, r, a, tok, bad);
 }
 
 template <int DT, int NP, bool ENT>
