@@ -248,6 +248,9 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
                     p.tok_logit[r] = l;
                     l = -INFINITY;
                 }
+                // Without mass, as the stage's ids this low are: times log2 e they may
+                // leave float32's range, and 2^y y would be 0 * -inf.  Keeps a NaN.
+                if (l <= kAbsentBelow) l = -INFINITY;
                 if (j < kHeld) {
                     sm.touched[s][walk.wid][j * 32 + lane] = l;
                 } else if (l != -INFINITY) {
