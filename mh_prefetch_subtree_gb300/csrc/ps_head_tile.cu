@@ -606,6 +606,12 @@ cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     if (n_ring > kMostRing) n_ring = kMostRing;
     const int smem = 1024 + fixed + n_ring * kRingBytes;
 
+    // First of all: in a thread that has used no CUDA before, this makes the device's
+    // context current, without which the driver refuses to make a map.
+    cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<U, N, C, ScaleT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+
     const EncodeTiled encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
     CUtensorMap map;
@@ -616,9 +622,6 @@ cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
 
-    cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<U, N, C, ScaleT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     const int64_t work = ((int64_t)p.head.V + kPipes * C * kTileRows - 1) / (kPipes * C * kTileRows) *
                          (((int64_t)p.n_rows + N - 1) / N);
     const int64_t clusters = sms / C;
