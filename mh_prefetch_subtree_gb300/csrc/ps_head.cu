@@ -406,9 +406,13 @@ cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     const int64_t tiles = ((int64_t)p.head.V + 16 * MT - 1) / (16 * MT);
     const int64_t cols = ((int64_t)p.n_rows + 8 * NT - 1) / (8 * NT);
     const int wk = split_k(tiles, cols, sms, K / 128, WARPS);
-    const int smem = NT * stage_k * 16 + (wk > 1 ? WARPS * 16 * MT * 8 * NT * 4 : 0);
+    constexpr int kJoin = WARPS * 16 * MT * 8 * NT * 4;
+    static_assert(kHeadSmem + kJoin <= 226 * 1024, "and 1 KB for what is static");
+    const int smem = NT * stage_k * 16 + (wk > 1 ? kJoin : 0);
+    // The most of any call: the limit belongs to the kernel, which calls with other sizes
+    // may be launching from other threads.
     cudaError_t e = cudaFuncSetAttribute(head_rows_kernel<U, NT, MT, WARPS, ScaleT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kHeadSmem + kJoin);
     if (e != cudaSuccess) return e;
     const int64_t per = WARPS / wk, work = (tiles + per - 1) / per * cols;
     head_rows_kernel<U, NT, MT, WARPS, ScaleT>

@@ -47,6 +47,7 @@ constexpr int kMostRing = 8, kMostWeights = 3, kMostSums = 4;
 constexpr int kTileWarps = 9 * kPipes + 1, kTileThreads = kTileWarps * 32;
 constexpr int kBytesB = 128 * 1024;                           // of hidden rows, at most
 constexpr int kSmemB = 227 * 1024;
+constexpr int kSmemStatic = 2 * 1024;                         // what is not dynamic, at most
 constexpr int kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -601,15 +602,17 @@ Shape shape_of(const HeadParams &p) {
 template <int U, int N, int C, typename ScaleT>
 cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     const int K = p.head.K, fixed = N / C * 2 * K;
-    // static shared memory and the alignment of the ring take less than 3 KB
-    int n_ring = (kSmemB - 3 * 1024 - fixed) / kRingBytes;
+    // 1 KB aligns the ring
+    int n_ring = (kSmemB - kSmemStatic - 1024 - fixed) / kRingBytes;
     if (n_ring > kMostRing) n_ring = kMostRing;
     const int smem = 1024 + fixed + n_ring * kRingBytes;
 
     // First of all: in a thread that has used no CUDA before, this makes the device's
-    // context current, without which the driver refuses to make a map.
+    // context current, without which the driver refuses to make a map.  The most of any
+    // call: the limit belongs to the kernel, which calls with other sizes may be launching
+    // from other threads.
     cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<U, N, C, ScaleT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemB - kSmemStatic);
     if (e != cudaSuccess) return e;
 
     const EncodeTiled encode = encode_tiled();
