@@ -172,6 +172,17 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
             : "memory");
 }
 
+// The same in this block alone.
+template <int C>
+__device__ __forceinline__ void tc_commit_here(uint64_t *bar) {
+    if constexpr (C == 1)
+        tc_commit<1>(bar);
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_addr(bar))
+                     : "memory");
+}
+
 // One thread of the warp.
 __device__ __forceinline__ bool elect() {
     uint32_t one;
@@ -554,8 +565,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const uint32_t turns = copy.turn + (i < copy.at);
                 if (turns > 0) drain(&bars.full[i], (turns - 1) & 1);
             }
-        if (wid >= 8 * kPipes && wid < 9 * kPipes) {
-            tc_commit<C>(&bars.drained[wid - 8 * kPipes]);
+        // the products, in the block that issues them; the arrival is at its own barrier,
+        // as the other block may be gone by the time that one there would come
+        if (wid >= 8 * kPipes && wid < 9 * kPipes && rank == 0) {
+            tc_commit_here<C>(&bars.drained[wid - 8 * kPipes]);
             drain(&bars.drained[wid - 8 * kPipes], 0);
         }
     }
