@@ -631,6 +631,18 @@ typedef struct {
 ps_status ps_head_rows(const ps_head *head, const void *hidden, int64_t hidden_ld, int32_t n_rows,
                        void *logits, int64_t ld, int32_t dtype, void *cuda_stream);
 
+/*
+ * Diagnostic, not a step of the method: ps_head_rows in the many-row kernel, whose
+ * first block leaves out the weight copies of its later tiles, as if they never
+ * landed, and gives up the waits for them after 5 ms (the other waits: 0.1 s).
+ * Logits are those of ps_head_rows or NaN, and NaN wherever the copies were left out.
+ * n_rows 33 to 64, K 256 to 2048, group 128 or more, bfloat16 scales; V of more than
+ * 256 rows for each multiprocessor, or the first block has no later tiles.
+ */
+ps_status ps_selftest_head_wait(const ps_head *head, const void *hidden, int64_t hidden_ld,
+                                int32_t n_rows, void *logits, int64_t ld, int32_t dtype,
+                                void *cuda_stream);
+
 /* Static text for a status code. */
 const char *ps_status_string(ps_status status);
 

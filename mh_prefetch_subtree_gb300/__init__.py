@@ -167,6 +167,8 @@ def lib() -> ctypes.CDLL:
         L.ps_head_rows.argtypes = [ctypes.POINTER(PsHead), _vp, ctypes.c_int64, ctypes.c_int32,
                                    _vp, ctypes.c_int64, ctypes.c_int32, _vp]
         L.ps_head_rows.restype = ctypes.c_int
+        L.ps_selftest_head_wait.argtypes = L.ps_head_rows.argtypes
+        L.ps_selftest_head_wait.restype = ctypes.c_int
         L.ps_status_string.argtypes = [ctypes.c_int]
         L.ps_status_string.restype = ctypes.c_char_p
         L.ps_version.argtypes = []
@@ -361,20 +363,31 @@ def ps_score_rows_rules(batch: PsSubtreeBatch, rules: PsLogitRules, lp0: torch.T
     return st
 
 
-def ps_head_rows(head: PsHead, hidden: torch.Tensor, logits: torch.Tensor, stream=None,
-                 check: bool = True) -> int:
-    """logits[:, :V] = hidden times the 4-bit head (see include/ps.h): hidden is
-    [n_rows, >= K] bfloat16, logits [n_rows, ld] bfloat16 or float32."""
+def _head_call(name: str, head: PsHead, hidden: torch.Tensor, logits: torch.Tensor, stream,
+               check: bool) -> int:
     _need(hidden, torch.bfloat16, "hidden")
     dt = _row_dtype(logits, "logits")
     shape, out_shape = hidden.shape, logits.shape
     if len(shape) != 2 or len(out_shape) != 2 or out_shape[0] != shape[0]:
         raise ValueError("hidden and logits must be matrices with the same number of rows")
-    st = (_lib or lib()).ps_head_rows(head, _ptr(hidden), shape[1], shape[0], _ptr(logits),
+    st = getattr(_lib or lib(), name)(head, _ptr(hidden), shape[1], shape[0], _ptr(logits),
                                       out_shape[1], dt, _stream(stream, logits))
     if check and st != PS_OK:
-        raise PsError(st, "ps_head_rows")
+        raise PsError(st, name)
     return st
+
+
+def ps_head_rows(head: PsHead, hidden: torch.Tensor, logits: torch.Tensor, stream=None,
+                 check: bool = True) -> int:
+    """logits[:, :V] = hidden times the 4-bit head (see include/ps.h): hidden is
+    [n_rows, >= K] bfloat16, logits [n_rows, ld] bfloat16 or float32."""
+    return _head_call("ps_head_rows", head, hidden, logits, stream, check)
+
+
+def ps_selftest_head_wait(head: PsHead, hidden: torch.Tensor, logits: torch.Tensor, stream=None,
+                          check: bool = True) -> int:
+    """Diagnostic: the many-row head kernel with weight copies left out (see include/ps.h)."""
+    return _head_call("ps_selftest_head_wait", head, hidden, logits, stream, check)
 
 
 def make_carry_io(*, state_seg, row_lp0, row_lq, next_lp0, next_lq, status, row_entropy=None,

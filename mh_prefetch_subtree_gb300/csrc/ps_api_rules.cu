@@ -51,6 +51,34 @@ ScoreWs score_ws(const ps_subtree_batch *b) {
     return w;
 }
 
+// What the host can see of a head's call; its parameters, for n_rows > 0.
+ps_status head_params(const ps_head *h, const void *hidden, int64_t hidden_ld, int32_t n_rows, void *logits,
+                      int64_t ld, int32_t dtype, HeadParams *p, int *sms) {
+    if (!h || n_rows < 0 || h->V < 1 || h->K < 1) return PS_ERR_INVALID_ARG;
+    if (elem_size(h->scale_dtype) == 0 || elem_size(dtype) == 0) return PS_ERR_UNSUPPORTED;
+    if (h->group != 32 && h->group != 64 && (h->group < 128 || h->group % 128 != 0))
+        return PS_ERR_UNSUPPORTED;
+    if (h->K % h->group != 0 || !h->q || !h->scales || !aligned(h->q, 16) ||
+        !aligned(h->scales, (size_t)elem_size(h->scale_dtype)))
+        return PS_ERR_INVALID_ARG;
+    if (n_rows == 0) return PS_OK;
+    if (!hidden || !aligned(hidden, 16) || hidden_ld < h->K || hidden_ld % 8 != 0 ||
+        hidden_ld > (int64_t(1) << 40))
+        return PS_ERR_INVALID_ARG;
+    ps_status st = check_rows_layout(logits, h->V, dtype, ld);
+    if (st != PS_OK) return st;
+    st = device_of(logits, sms);
+    if (st != PS_OK) return st;
+    p->head = *h;
+    p->hidden = (const uint16_t *)hidden;
+    p->hidden_ld = hidden_ld;
+    p->n_rows = n_rows;
+    p->logits = logits;
+    p->ld = ld;
+    p->dtype = dtype;
+    return PS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -140,31 +168,23 @@ ps_status ps_score_rows_rules(const ps_subtree_batch *b, const ps_logit_rules *r
 
 ps_status ps_head_rows(const ps_head *h, const void *hidden, int64_t hidden_ld, int32_t n_rows,
                        void *logits, int64_t ld, int32_t dtype, void *cuda_stream) {
-    if (!h || n_rows < 0 || h->V < 1 || h->K < 1) return PS_ERR_INVALID_ARG;
-    if (elem_size(h->scale_dtype) == 0 || elem_size(dtype) == 0) return PS_ERR_UNSUPPORTED;
-    if (h->group != 32 && h->group != 64 && (h->group < 128 || h->group % 128 != 0))
-        return PS_ERR_UNSUPPORTED;
-    if (h->K % h->group != 0 || !h->q || !h->scales || !aligned(h->q, 16) ||
-        !aligned(h->scales, (size_t)elem_size(h->scale_dtype)))
-        return PS_ERR_INVALID_ARG;
-    if (n_rows == 0) return PS_OK;
-    if (!hidden || !aligned(hidden, 16) || hidden_ld < h->K || hidden_ld % 8 != 0 ||
-        hidden_ld > (int64_t(1) << 40))
-        return PS_ERR_INVALID_ARG;
-    ps_status st = check_rows_layout(logits, h->V, dtype, ld);
-    if (st != PS_OK) return st;
-    int sms = 0;
-    st = device_of(logits, &sms);
-    if (st != PS_OK) return st;
     HeadParams p{};
-    p.head = *h;
-    p.hidden = (const uint16_t *)hidden;
-    p.hidden_ld = hidden_ld;
-    p.n_rows = n_rows;
-    p.logits = logits;
-    p.ld = ld;
-    p.dtype = dtype;
+    int sms = 0;
+    const ps_status st = head_params(h, hidden, hidden_ld, n_rows, logits, ld, dtype, &p, &sms);
+    if (st != PS_OK || n_rows == 0) return st;
     return map_cuda(launch_head_rows(p, sms, (cudaStream_t)cuda_stream));
+}
+
+ps_status ps_selftest_head_wait(const ps_head *h, const void *hidden, int64_t hidden_ld, int32_t n_rows,
+                                void *logits, int64_t ld, int32_t dtype, void *cuda_stream) {
+    if (!h || n_rows < 33 || n_rows > 64 || h->K < 256 || h->K > 2048 || h->group < 128 ||
+        h->scale_dtype != PS_BF16)
+        return PS_ERR_INVALID_ARG;
+    HeadParams p{};
+    int sms = 0;
+    const ps_status st = head_params(h, hidden, hidden_ld, n_rows, logits, ld, dtype, &p, &sms);
+    if (st != PS_OK) return st;
+    return map_cuda(launch_head_lost(p, sms, (cudaStream_t)cuda_stream));
 }
 
 }  // extern "C"

@@ -76,5 +76,8 @@ __device__ __forceinline__ uint4 hidden_pairs(uint4 h, float2 e) {
 cudaError_t launch_head_rows(const HeadParams &p, int sms, cudaStream_t stream);
 bool head_tile_takes(const HeadParams &p, int sms);
 cudaError_t launch_head_tile(const HeadParams &p, int sms, cudaStream_t stream);
+// ps_selftest_head_wait: 33 to 64 hidden rows of at most 2048 elements, bfloat16 scales,
+// groups of 128 or more.
+cudaError_t launch_head_lost(const HeadParams &p, int sms, cudaStream_t stream);
 
 }  // namespace ps

@@ -30,8 +30,8 @@
 // the time with groups of 64, the issue slots 54%.  (16 rows at a time took 116 us for
 // 151936 x 4096 where ps_head.cu takes 92.)
 //
-// Every wait is bounded; where one runs out, the block goes on without waiting and
-// stores NaN for what it could not make.
+// Every wait is bounded.  Where one runs out, nothing more is handed on, the waits after
+// it run out too, and NaN is stored for what could not be made.
 #include <cuda.h>
 
 #include "ps_head.cuh"
@@ -50,12 +50,23 @@ constexpr int kSmemB = 227 * 1024;
 constexpr int kSmemStatic = 2 * 1024;                         // what is not dynamic, at most
 constexpr int kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint64_t kTestWaitNs = 100000000ull;                // in the diagnostic variant
+
+// A place in a ring, and how often it has gone round.
+struct Place {
+    uint32_t at, turn;
+    __device__ __forceinline__ void step(uint32_t by, uint32_t ring) {
+        at += by;
+        if (at >= ring) at -= ring, ++turn;
+    }
+};
 
 struct TileBars {
     uint64_t full[kMostRing], empty[kMostRing];               // the ring of copies
     uint64_t made[kPipes][kMostWeights], freed[kPipes][kMostWeights];
     uint64_t done[kPipes][kMostSums], taken[kPipes][kMostSums];
     uint64_t drained[kPipes];
+    Place issued;                                             // of the last copy
     uint32_t tmem;
     int failed;
 };
@@ -93,7 +104,8 @@ __device__ __forceinline__ void sync_all() {
 }
 
 // A bounded wait; once one of the block has run out, none waits any more.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *failed) {
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *failed,
+                                     uint64_t limit_ns = kWaitNs) {
     uint64_t t0 = 0;
     for (uint32_t i = 1; i < (1u << 28); ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -101,7 +113,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
         if ((i & 255u) == 0) {
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
-            if (*failed || now - t0 > kWaitNs) break;
+            if (*failed || now - t0 > limit_ns) break;
         }
     }
     *failed = 1;
@@ -234,16 +246,9 @@ struct Scales<float> {
     }
 };
 
-// A place in a ring, and how often it has gone round.
-struct Place {
-    uint32_t at, turn;
-    __device__ __forceinline__ void step(uint32_t by, uint32_t ring) {
-        at += by;
-        if (at >= ring) at -= ring, ++turn;
-    }
-};
-
-template <int U, int N, int C, typename ScaleT>
+// LOST (a diagnostic): the first block leaves out the weight copies of all its tiles but
+// the first of each pipeline and soon gives up the waits for them; the others are short.
+template <int U, int N, int C, typename ScaleT, bool LOST>
 __global__ void __launch_bounds__(kTileThreads, 1)
     head_tile_kernel(const HeadParams p, const int n_ring, const __grid_constant__ CUtensorMap map) {
     extern __shared__ uint8_t smem_raw[];
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int kHere = N / C;                                // hidden rows in this block
     __shared__ float2 scale_to[kHere], scale_back[N];           // powers of two, as two factors
     volatile int *failed = &bars.failed;
+    constexpr uint64_t kLimit = LOST ? kTestWaitNs : kWaitNs;
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     uint8_t *ring = smem;                                       // [ring][128 rows][128 B], swizzled
     uint4 *hid = reinterpret_cast<uint4 *>(smem + n_ring * kRingBytes);       // [k / 8][N]
@@ -282,6 +288,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int i = 0; i < kPipes; ++i) mbar_init(&bars.drained[i], 1);
         bars.failed = 0;
+        bars.issued = Place{0, 0};
         fence_mbar_init();
     }
     if (wid == 8 * kPipes) {
@@ -339,20 +346,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         asm volatile("fence.proxy.async;" ::: "memory");
         sync_all<C>();
+        // Once a wait has run out its role hands nothing on any more, so that the waits that
+        // depend on it run out as well, and in the end those for sums.
+        bool ok = __all_sync(0xffffffffu, !*failed);
 
         if (wid == 9 * kPipes) {
             // the producer
             if (lane == 0) {
-                bool ok = true;
                 for (int64_t pair = pair0; pair < n_pairs; pair += pair_step)
                     for (int s = 0; s < n_steps; ++s)
                         for (int pipe = 0; pipe < kPipes; ++pipe, copy.step(1, n_ring)) {
                             const uint32_t slot = copy.at;
-                            if (copy.turn > 0) ok = ok && wait(&bars.empty[slot], (copy.turn - 1) & 1, failed);
-                            if (!ok) continue;
+                            if (copy.turn > 0) ok = ok && wait(&bars.empty[slot], (copy.turn - 1) & 1, failed, kLimit);
+                            if (!ok || (LOST && blockIdx.x == 0 && pair != pair0)) continue;
                             mbar_arrive_expect_tx(&bars.full[slot], kRingBytes);
                             tma_2d(smem_addr(ring + slot * kRingBytes), &map, s * kStepBytes, (int32_t)first_row(pair, pipe),
                                    &bars.full[slot]);
+                            bars.issued = copy;
                         }
             }
         } else if (wid >= 8 * kPipes) {
@@ -363,12 +373,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const uint64_t desc0 = (uint64_t)1 << 46 | (uint64_t)(128 >> 4) << 32 | (uint64_t)kHere << 16;
             // 14 bits: in a cluster an address has the rank of the block above them
             const uint32_t hid_at = smem_addr(hid) >> 4 & 0x3fffu;
-            bool ok = true;
             const int pipe = wid - 8 * kPipes;
             for (int64_t pair = rank ? n_pairs : pair0; pair < n_pairs; pair += pair_step)
                 for (int u = 0; u < n_units; ++u, weights.step(1, kA), sums.step(1, kD)) {
-                    if (sums.turn > 0) ok = ok && wait(&bars.taken[pipe][sums.at], (sums.turn - 1) & 1, failed);
-                    ok = ok && wait(&bars.made[pipe][weights.at], weights.turn & 1, failed);
+                    if (sums.turn > 0) ok = ok && wait(&bars.taken[pipe][sums.at], (sums.turn - 1) & 1, failed, kLimit);
+                    ok = ok && wait(&bars.made[pipe][weights.at], weights.turn & 1, failed, kLimit);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) continue;
                     tc_after();
@@ -390,7 +399,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int groups = K / p.head.group;
             const uint32_t per_group = U == 128 ? p.head.group / 128 : 1;
             const bool wide = per_group == 1 && groups % 8 == 0 && (reinterpret_cast<uintptr_t>(p.head.zeros) & 7) == 0;
-            bool ok = true;
             uint32_t z[2], next[2] = {0x08080808u, 0x08080808u};
             auto fetch = [&](int64_t pair, int u0) {
                 if (!p.head.zeros) return;
@@ -406,8 +414,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             };
             if (pair0 < n_pairs) fetch(pair0, 0);
-            for (int64_t pair = pair0; pair < n_pairs; pair += pair_step) {
-                for (int u0 = 0; u0 < n_units; u0 += 8) {
+            for (int64_t pair = pair0; ok && pair < n_pairs; pair += pair_step) {
+                for (int u0 = 0; ok && u0 < n_units; u0 += 8) {
                     z[0] = next[0], z[1] = next[1];
                     if (u0 + 8 < n_units)
                         fetch(pair, u0 + 8);
@@ -418,10 +426,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int i = 0; i < n_now; ++i) {
                         const int u = u0 + i;
                         const uint32_t at = copy.at;
-                        if (i % kUnitsStep == 0) ok = ok && wait(&bars.full[at], copy.turn & 1, failed);
+                        if (LOST && blockIdx.x == 0 && pair != pair0) {
+                            // all four warps at once, so that the others have had no time to see it
+                            const uint64_t t0 = global_timer_ns();
+                            while (global_timer_ns() - t0 < kTestWaitNs / 20) {}
+                            *failed = 1, ok = false;
+                        }
+                        if (i % kUnitsStep == 0) ok = ok && wait(&bars.full[at], copy.turn & 1, failed, kLimit);
                         const uint32_t slot = weights.at;
-                        if (weights.turn > 0) ok = ok && wait(&bars.freed[pipe][slot], (weights.turn - 1) & 1, failed);
-                        __syncwarp();
+                        if (weights.turn > 0) ok = ok && wait(&bars.freed[pipe][slot], (weights.turn - 1) & 1, failed, kLimit);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
                         tc_after();
                         const uint32_t zero = z[0] & 15u;
                         z[0] = __funnelshift_r(z[0], z[1], 8);
@@ -467,7 +482,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int groups = K / p.head.group;
             const uint32_t per_group = U == 128 ? p.head.group / 128 : 1;
             const bool wide = per_group == 1 && groups % 8 == 0 && (reinterpret_cast<uintptr_t>(p.head.scales) & 15) == 0;
-            bool ok = true;
             Scales<ScaleT> held, next;
             auto fetch = [&](int64_t pair, int u0) {
                 const ScaleT *scales = reinterpret_cast<const ScaleT *>(p.head.scales) +
@@ -497,8 +511,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
                     for (int i = 0; i < n_now; ++i) {
                         const uint32_t slot = sums.at;
-                        ok = ok && wait(&bars.done[pipe][slot], sums.turn & 1, failed);
-                        __syncwarp();
+                        ok = ok && wait(&bars.done[pipe][slot], sums.turn & 1, failed, kLimit);
+                        ok = __all_sync(0xffffffffu, ok);
                         tc_after();
                         const float s = held.take();
                         uint64_t ss;
@@ -515,7 +529,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                                 if (h == N / 32 - 1 && c == 1) {      // all are in registers
                                     tc_before();
                                     __syncwarp();
-                                    if (lane == 0) {
+                                    if (lane == 0 && ok) {
                                         if (C == 1) arrive(&bars.taken[pipe][slot]);
                                         else arrive_at(&bars.taken[pipe][slot], 0);
                                     }
@@ -554,20 +568,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     // The sums of all products have been taken in, so nothing is in flight; after a
     // wait that ran out, copies and products may be, and are waited for.
-    if (*failed && lane == 0) {
+    if (__any_sync(0xffffffffu, *failed)) {
         auto drain = [&](uint64_t *bar, uint32_t parity) {
             const uint64_t t0 = global_timer_ns();
             while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitNs / 100) {}
         };
-        if (wid == 9 * kPipes)
+        if (wid == 9 * kPipes && lane == 0)
             for (uint32_t i = 0; i < (uint32_t)n_ring; ++i) {
-                // the last copy into a place: of this turn, or of the one before
-                const uint32_t turns = copy.turn + (i < copy.at);
+                // the last copy into a place: of the last copy's turn, or of the one before
+                const uint32_t turns = bars.issued.turn + (i <= bars.issued.at);
                 if (turns > 0) drain(&bars.full[i], (turns - 1) & 1);
             }
-        // the products, in the block that issues them; the arrival is at its own barrier,
-        // as the other block may be gone by the time that one there would come
-        if (wid >= 8 * kPipes && wid < 9 * kPipes && rank == 0) {
+        // the products, by the thread that issues them; the arrival is at its own block's
+        // barrier, as the other block may be gone by the time that one there would come
+        if (wid >= 8 * kPipes && wid < 9 * kPipes && rank == 0 && elect()) {
             tc_commit_here<C>(&bars.drained[wid - 8 * kPipes]);
             drain(&bars.drained[wid - 8 * kPipes], 0);
         }
@@ -612,7 +626,7 @@ Shape shape_of(const HeadParams &p) {
     return Shape{0, 0};
 }
 
-template <int U, int N, int C, typename ScaleT>
+template <int U, int N, int C, typename ScaleT, bool LOST = false>
 cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     const int K = p.head.K, fixed = N / C * 2 * K;
     // 1 KB aligns the ring
@@ -624,7 +638,7 @@ cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     // context current, without which the driver refuses to make a map.  The most of any
     // call: the limit belongs to the kernel, which calls with other sizes may be launching
     // from other threads.
-    cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<U, N, C, ScaleT>,
+    cudaError_t e = cudaFuncSetAttribute(head_tile_kernel<U, N, C, ScaleT, LOST>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemB - kSmemStatic);
     if (e != cudaSuccess) return e;
 
@@ -652,7 +666,7 @@ cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, head_tile_kernel<U, N, C, ScaleT>, p, n_ring, map);
+    return cudaLaunchKernelEx(&cfg, head_tile_kernel<U, N, C, ScaleT, LOST>, p, n_ring, map);
 }
 
 template <int U, typename ScaleT>
@@ -692,6 +706,11 @@ cudaError_t launch_head_tile(const HeadParams &p, int sms, cudaStream_t stream) 
     if (p.head.group == 32) return launch_u<32>(p, sms, stream);
     if (p.head.group == 64) return launch_u<64>(p, sms, stream);
     return launch_u<128>(p, sms, stream);
+}
+
+cudaError_t launch_head_lost(const HeadParams &p, int sms, cudaStream_t stream) {
+    return shape_of(p).blocks == 1 ? launch<128, 64, 1, uint16_t, true>(p, sms, stream)
+                                   : launch<128, 64, 2, uint16_t, true>(p, sms, stream);
 }
 
 }  // namespace ps
