@@ -582,7 +582,8 @@ ps_status ps_process_rows(const ps_logit_rules *rules, int32_t V, int32_t dtype,
  * ps_score_rows; logits in masked places are not looked at.
  * workspace  device memory, 256-byte aligned, >= ps_rules_workspace_bytes(batch):
  *            partial sums of every row's vocabulary slices (depends on V, dtype
- *            and n_rows).
+ *            and n_rows, and never falls as n_rows rises: the size for the largest
+ *            batch is enough for all smaller ones).
  * The results feed ps_assemble_subtree as those of ps_score_rows do.
  */
 size_t ps_rules_workspace_bytes(const ps_subtree_batch *batch);

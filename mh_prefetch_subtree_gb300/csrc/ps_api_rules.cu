@@ -35,7 +35,8 @@ ps_status check_rules_host(const ps_logit_rules *u, int32_t V, int64_t n_rows) {
     return PS_OK;
 }
 
-// Workspace of ps_score_rows_rules.
+// Workspace of ps_score_rows_rules.  Its size is what the most demanding batch of up to
+// as many rows takes, so that one for the largest batch serves all.
 struct ScoreWs {
     RuleCut cut;
     size_t tok_off, bad_off, total;
@@ -47,7 +48,8 @@ ScoreWs score_ws(const ps_subtree_batch *b) {
     const size_t n = (size_t)b->n_rows;
     w.tok_off = align_up(n * w.cut.n_slices * kScoreParts * sizeof(ChunkPart), kAlign);
     w.bad_off = w.tok_off + align_up(n * sizeof(float), kAlign);
-    w.total = w.bad_off + align_up(n * sizeof(int32_t), kAlign);
+    w.total = align_up((size_t)score_slices(b->V, b->dtype, b->n_rows) * kScoreParts * sizeof(ChunkPart), kAlign) +
+              align_up(n * sizeof(float), kAlign) + align_up(n * sizeof(int32_t), kAlign);
     return w;
 }
 

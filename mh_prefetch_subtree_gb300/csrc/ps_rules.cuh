@@ -33,6 +33,8 @@ struct RuleCut {
 // most: ids of a slice at most (a multiple of kSegIds).
 RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows);
 RuleCut score_cut(int32_t V, int32_t dtype, int64_t n_rows);
+// The slices of all rows together, of any batch of up to n_rows rows.
+int64_t score_slices(int32_t V, int32_t dtype, int64_t n_rows);
 constexpr int kScoreParts = 16;     // partial sums of a slice of a row: one a warp
 
 // Sums of one warp's ids of a slice (ps_row_sums.cuh has their meaning).

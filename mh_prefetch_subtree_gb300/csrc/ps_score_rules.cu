@@ -535,8 +535,9 @@ cudaError_t launch_np(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
 // bf16 without masks, 150 rows of 50021 float32 with long histories): none 764 and 109 us,
 // 2: 626 and 78, 9: 599 and 68, all: 611 and 65, but with masks, whose segments are
 // copied too, 9: 765 and all: 800.
+constexpr int64_t kBlocks = 152;
 RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows) {
-    constexpr int64_t kBlocks = 152, kHead = 9;
+    constexpr int64_t kHead = 9;
     int64_t n = kBlocks / (n_rows > 0 ? n_rows : 1);
     if (n > V / 1024) n = V / 1024;
     if (n < 1) n = 1;
@@ -554,8 +555,21 @@ RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows) {
     }
 }
 
+static int32_t score_most(int32_t dtype) {
+    return dtype == PS_BF16 ? ScoreSmem<PS_BF16>::kIds : ScoreSmem<PS_F32>::kIds;
+}
+
 RuleCut score_cut(int32_t V, int32_t dtype, int64_t n_rows) {
-    return rule_cut(V, dtype == PS_BF16 ? ScoreSmem<PS_BF16>::kIds : ScoreSmem<PS_F32>::kIds, n_rows);
+    return rule_cut(V, score_most(dtype), n_rows);
+}
+
+// A row has as few slices as hold the vocabulary, or so many that all rows together
+// have at most kBlocks; the latter would fall as rows are added, the bound rises.
+int64_t score_slices(int32_t V, int32_t dtype, int64_t n_rows) {
+    const int64_t few = n_rows * (((int64_t)V + score_most(dtype) - 1) / score_most(dtype));
+    const int64_t cut = n_rows * (V / 1024);
+    const int64_t many = cut < kBlocks ? cut : kBlocks;
+    return few > many ? few : many;
 }
 
 cudaError_t launch_score_rules(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
