@@ -85,6 +85,7 @@ class PsLogitRules(ctypes.Structure):
         [(n, _vp) for n in ("seq_begin", "seq_tokens", "seq_prompt", "repetition", "frequency",
                             "presence", "bias_begin", "bias_ids", "bias_values", "mask",
                             "row_seq", "row_len", "row_mask")]
+    _rows = None        # rows that the row arrays hold, where make_rules has seen them
 
 
 class PsHead(ctypes.Structure):
