@@ -48,6 +48,15 @@ namespace ps {
 
 int elem_size(int32_t dtype) { return dtype == PS_BF16 ? 2 : (dtype == PS_F32 ? 4 : 0); }
 
+bool on_device(const void *ptr) {
+    cudaPointerAttributes attr;
+    if (cudaPointerGetAttributes(&attr, ptr) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return attr.type == cudaMemoryTypeDevice || attr.type == cudaMemoryTypeManaged;
+}
+
 // Device that owns `ptr`, made current for this thread; SM count cached.
 ps_status device_of(const void *ptr, int *sms) {
     cudaPointerAttributes attr;

@@ -16,6 +16,8 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Bytes of an element of a ps_dtype; 0 for any other value.
 int elem_size(int32_t dtype);
+// Whether `ptr` is memory that kernels may be given: a device's, or managed.
+bool on_device(const void *ptr);
 // Makes the device that owns `ptr` current; its SM count.
 ps_status device_of(const void *ptr, int *sms);
 ps_status map_cuda(cudaError_t e);

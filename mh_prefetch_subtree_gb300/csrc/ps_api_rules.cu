@@ -69,6 +69,7 @@ ps_status head_params(const ps_head *h, const void *hidden, int64_t hidden_ld, i
         return PS_ERR_INVALID_ARG;
     ps_status st = check_rows_layout(logits, h->V, dtype, ld);
     if (st != PS_OK) return st;
+    if (!on_device(hidden) || !on_device(h->q)) return PS_ERR_INVALID_ARG;
     st = device_of(logits, sms);
     if (st != PS_OK) return st;
     p->head = *h;
@@ -105,6 +106,7 @@ ps_status ps_process_rows(const ps_logit_rules *rules, int32_t V, int32_t dtype,
     const int64_t na = ((n_rows - 1) * ld + V) * esz, nb = ((n_rows - 1) * out_ld + V) * esz;
     if (a == b ? ld != out_ld : (a < b + nb && b < a + na)) return PS_ERR_INVALID_ARG;
     int sms = 0;
+    if (a != b && !on_device(logits)) return PS_ERR_INVALID_ARG;
     st = device_of(out, &sms);
     if (st != PS_OK) return st;
     ProcessParams p{};
