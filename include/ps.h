@@ -514,6 +514,7 @@ ps_status ps_selftest_read(const void *data, size_t bytes, uint32_t *sink, void 
  * n_seqs        number of sequences, >= 0.
  * seq_begin     [n_seqs+1] CSR offsets into seq_tokens, or NULL: no history, so
  *               no penalties (the five arrays down to presence are then not read).
+ *               A sequence has at most 2^31 - 1 tokens.
  * seq_tokens    [n_tokens] int32 ids.
  * seq_prompt    [n_seqs] or NULL (0): leading tokens that are the prompt, which
  *               count as seen and not as generated.

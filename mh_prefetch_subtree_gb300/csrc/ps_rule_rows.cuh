@@ -394,9 +394,9 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
             n >= n0 && n <= w.len_all && n - n0 <= kMaxNew) {
             n_new = n - n0;
             if (n_new) {
-                if (n0 < win || n > win + 32) {
+                if (n0 < win || n - 32 > win) {
                     win = n0;
-                    win_tok = win + lane < w.len_all ? __ldg(w.hist + win + lane) : 0;
+                    win_tok = lane < w.len_all - win ? __ldg(w.hist + win + lane) : 0;
                 }
                 const int32_t id = __shfl_sync(0xffffffffu, win_tok, (n0 - win + lane) & 31);
                 if (lane < n_new) {
@@ -493,20 +493,21 @@ __device__ __noinline__ const int32_t *rule_tables(Smem &sm, SliceMap map, const
     if (!rule_meet(sm, 3 * k + 1)) return nullptr;
     const bool fits = len - max(0, min(prompt, len)) < (int32_t)kCountFull;
     constexpr int kAhead = 8;                       // tokens that a thread asks for at once
-    for (int b = 0; b < len; b += kCountThreads * kAhead) {
+    // unsigned: a step past the last of 2^31 - 1 tokens has to end the loops
+    for (uint32_t b = 0; b < (uint32_t)len; b += kCountThreads * kAhead) {
         int32_t id[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int i = b + j * kCountThreads + tid;
-            id[j] = i < len ? __ldg(hist + i) : 0;
+            const uint32_t i = b + j * kCountThreads + tid;
+            id[j] = i < (uint32_t)len ? __ldg(hist + i) : 0;
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-            const int i = b + j * kCountThreads + tid;
-            if (i < len) count_token(sm, map, id[j], i >= prompt, fits, bad_word);
+            const uint32_t i = b + j * kCountThreads + tid;
+            if (i < (uint32_t)len) count_token(sm, map, id[j], (int32_t)i >= prompt, fits, bad_word);
         }
     }
-    for (int i = tid; i < w.n_bias; i += kCountThreads) {
+    for (uint32_t i = tid; i < (uint32_t)w.n_bias; i += kCountThreads) {
         const int32_t id = __ldg(w.bias_ids + i);
         if (id < 0 || id >= map.V || (i > 0 && id <= __ldg(w.bias_ids + i - 1))) {
             atomicOr(bad_word, PS_DEV_BAD_RULES);

@@ -147,7 +147,8 @@ __device__ int32_t build_table(SliceTable &t, const RowRules &w, int32_t V, int3
     t.seen[tid] = 0;
     __syncthreads();
     int bad_tok = 0, bad_bias = 0;
-    for (int i = tid; i < w.len; i += blockDim.x) {
+    // unsigned: a step past the last of 2^31 - 1 tokens has to end the loop
+    for (uint32_t i = tid; i < (uint32_t)w.len; i += blockDim.x) {
         const int32_t id = __ldg(w.hist + i);
         if (id < 0 || id >= V) {
             bad_tok = 1;
@@ -157,9 +158,9 @@ __device__ int32_t build_table(SliceTable &t, const RowRules &w, int32_t V, int3
         if (o >= (uint32_t)kSliceIds) continue;
         atomicOr(&t.count[o], kSeen);
         atomicOr(&t.seen[o % kTableThreads], 1u << (o / kTableThreads));
-        if (i >= w.prompt) atomicAdd(&t.count[o], 1u);
+        if ((int32_t)i >= w.prompt) atomicAdd(&t.count[o], 1u);
     }
-    for (int i = tid; i < w.n_bias; i += blockDim.x) {
+    for (uint32_t i = tid; i < (uint32_t)w.n_bias; i += blockDim.x) {
         const int32_t id = __ldg(w.bias_ids + i);
         if (id < 0 || id >= V || (i > 0 && id <= __ldg(w.bias_ids + i - 1))) {
             bad_bias = 1;
