@@ -436,6 +436,8 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
         if (mbar_wait_bounded(&sm.full[me], odd, kRuleDrainNs) &&
             mbar_wait_bounded(&sm.empty[me], odd, kRuleWaitNs))
             done(me, r_before, slice_before);
+        else if (lane == 0)
+            set_status(p.status, PS_DEV_TIMEOUT);              // the row is not stored
     }
 }
 
