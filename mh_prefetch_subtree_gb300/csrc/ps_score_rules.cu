@@ -248,12 +248,9 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
                     p.tok_logit[r] = l;
                     l = -INFINITY;
                 }
-                // Without mass, as the stage's ids this low are: times log2 e they may
-                // leave float32's range, and 2^y y would be 0 * -inf.  Keeps a NaN.
-                if (l <= kAbsentBelow) l = -INFINITY;
                 if (j < kHeld) {
                     sm.touched[s][walk.wid][j * 32 + lane] = l;
-                } else if (l != -INFINITY) {
+                } else if (!(l <= kAbsentBelow)) {
                     const float x = l * kLog2e;
                     if (!(x <= more.R)) more = rebase<NP, ENT>(more, x, g);       // keeps a NaN
                     const float y = x - more.R, e = ex2(y);
@@ -365,6 +362,9 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
         float px = -INFINITY;
         if ((uint32_t)(wid / kPatchWarps * 32 + lane) < (uint32_t)sm.n_touched[s][wid % kPatchWarps])
             px = sm.touched[s][wid % kPatchWarps][wid / kPatchWarps * 32 + lane];
+        // Without mass, as the stage's ids this low are: times log2 e it may leave float32's
+        // range, and 2^y y would be 0 * -inf.  Keeps a NaN.
+        if (px <= kAbsentBelow) px = -INFINITY;
         Sums sum{0.f, 0.f, 0.f};
         auto join_lanes = [&](Sums a) {
             if (px != -INFINITY) add_term<NP, ENT>(a, fmaf(px, kLog2e, -ref), g);
@@ -458,14 +458,33 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
     }
 }
 
-// Empties a part whose exponentials are 0 next to those of reference M, under tau as well.
-// (A part of logits like -1e12 has sums of no meaning: a product's rounding is 2^16 there,
-// so they may be infinite, and infinity times 0 would be NaN.)  Keeps NaN.
-__device__ __forceinline__ void drop_far(Acc &a, float M, float far) {
-    if (a.R < M - far) a = acc_empty();
+// A row's parts, joined in their order by one warp; the result is in all lanes.
+// FAR: parts whose exponentials are 0 next to those of the row's largest logit, under tau
+// as well, are left out.
+template <int NP, bool ENT, bool FAR>
+__device__ __forceinline__ Acc join_parts(const ChunkPart *parts, int n, float tok, float g) {
+    const int lane = threadIdx.x & 31;
+    float least = -INFINITY;
+    if constexpr (FAR) {
+        float top = tok * kLog2e;                     // the sums leave the token out
+        for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(&parts[i].R));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        least = top - 2048.f / fminf(g, 1.f);
+    }
+    Acc a = acc_empty();
+    for (int i = lane; i < n; i += 32) {
+        const float4 s = __ldcg(reinterpret_cast<const float4 *>(parts + i));
+        if (FAR && s.x < least) continue;
+        a = merge_part<NP, ENT>(a, Acc{s.x, s.y, {s.z, 0.f, 0.f}, s.w}, g);
+    }
+    return warp_merge<NP, ENT>(a, g);
 }
 
-// One warp a row: its partial sums joined in their order, then the results.
+// One warp a row: its partial sums joined, then the results.  A part of logits like -1e12
+// has sums of no meaning (a product's rounding is 2^16 there): they may be infinite, and
+// infinity times the 0 that it counts for next to others is NaN.  So sums that are not
+// finite are formed again without such parts.
 template <int NP, bool ENT>
 __global__ void __launch_bounds__(256) score_rules_join_kernel(
     const __grid_constant__ ScoreRulesParams p) {
@@ -474,23 +493,12 @@ __global__ void __launch_bounds__(256) score_rules_join_kernel(
     if (r >= p.r.n_rows) return;
     pdl_wait_prerequisites();                         // launched while the sums are made
     const bool bad = p.row_bad[r] != 0;
-    const int n = p.cut.n_slices * kScoreParts;
-    const float far = 2048.f / fminf(p.rows.g, 1.f);
-    Acc a = acc_empty();
-    if (!bad)
-        for (int i = lane; i < n; i += 32) {
-            const float4 s = __ldcg(reinterpret_cast<const float4 *>(p.parts + r * n + i));
-            Acc b{s.x, s.y, {s.z, 0.f, 0.f}, s.w};
-            drop_far(a, b.R, far);
-            drop_far(b, a.R, far);
-            a = merge_part<NP, ENT>(a, b, p.rows.g);
-        }
-    const float tok = bad ? 0.f : p.tok_logit[r];
-    float top = fmaxf(a.R, tok * kLog2e);             // the sums leave the token out
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    drop_far(a, top, far);
-    a = warp_merge<NP, ENT>(a, p.rows.g);
+    const float g = p.rows.g, tok = bad ? 0.f : p.tok_logit[r];
+    const int n = bad ? 0 : p.cut.n_slices * kScoreParts;
+    const ChunkPart *parts = p.parts + r * p.cut.n_slices * kScoreParts;
+    Acc a = join_parts<NP, ENT, false>(parts, n, tok, g);
+    const bool finite = finite_f(a.s1) && (NP == 1 || finite_f(a.st[0])) && (!ENT || finite_f(a.y1));
+    if (__any_sync(0xffffffffu, !finite)) a = join_parts<NP, ENT, true>(parts, n, tok, g);
     if (lane == 0) finalize_row<NP, ENT>(p.rows, r, a, tok, bad);
 }
 
