@@ -222,12 +222,11 @@ struct RuleSpan {
     }
 };
 
-// A producer warp: fills stage `me` with every RING-th row.
-// SPARSE: where a row's mask leaves few of the slice's ids, only the 16-byte
-// vectors that hold one are copied.
+// A producer warp: fills stage `me` with every RING-th row.  Where a row's mask leaves few
+// of the slice's ids, only the 16-byte vectors that hold one are copied.
 // done(row, slice): called once the consumers have finished the stage's row, before
 // the stage is filled again.
-template <int DT, int NB, int RING, bool SPARSE, typename Done>
+template <int DT, int NB, int RING, typename Done>
 __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const RulesParams &p,
                                               const RuleCut &cut, const uint8_t *logits,
                                               int64_t ld_bytes,
@@ -308,13 +307,13 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
         const uint32_t *mrow = u.mask + (masked ? rm * u.mask_ld : 0);
         const uint64_t key = (uint64_t)(rm * cut.n_slices + map.slice) + 1;
         bool known = false;
-        if (SPARSE && masked) {
+        if (masked) {
             const uint64_t x = *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache];
             known = x >> 16 == key;
             if (known && (int32_t)(x & 0xffffu) * 16 * kSparseShare <= (int32_t)bytes) flags |= kDescSparse;
         }
         const bool sparse = flags & kDescSparse;
-        const bool copy_mask = masked && mask16 && !sparse && (known || !SPARSE);   // in bulk too
+        const bool copy_mask = masked && mask16 && !sparse && known;    // in bulk too
         if (!sparse) {
             if (lane == 0) {
                 fence_proxy_async_smem();
@@ -356,11 +355,11 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
                     make_uint4(m[i], m[i + 1], m[i + 2], m[i + 3]);
                 ids += __popc(m[i]) + __popc(m[i + 1]) + __popc(m[i + 2]) + __popc(m[i + 3]);
             }
-            if (SPARSE && !known) {
+            if (!known) {
                 ids = __reduce_add_sync(0xffffffffu, ids);
                 if (lane == 0) *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache] = key << 16 | ids;
             }
-            if (SPARSE && sparse) {
+            if (sparse) {
                 fence_proxy_async_smem();
 #pragma unroll
                 for (int i = 0; i < kWpl; ++i) {

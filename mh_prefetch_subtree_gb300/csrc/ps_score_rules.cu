@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
     __syncthreads();
 
     if (wid >= kFirstProducer) {
-        rule_producer<DT, kNb, kRing, true>(sm, p.r, p.cut, p.rows.logits, p.rows.ld_bytes,
+        rule_producer<DT, kNb, kRing>(sm, p.r, p.cut, p.rows.logits, p.rows.ld_bytes,
                                             p.rows.row_index, p.rows.n_logit_rows,
                                             p.rows.tokens, [](int, int64_t, int32_t) {});
         return;
@@ -543,6 +543,8 @@ cudaError_t launch_np(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
 // bf16 without masks, 150 rows of 50021 float32 with long histories): none 764 and 109 us,
 // 2: 626 and 78, 9: 599 and 68, all: 611 and 65, but with masks, whose segments are
 // copied too, 9: 765 and all: 800.
+// The blocks to cut for are a constant, and not the device's own multiprocessors (152 on a
+// GB300), so that a workspace's size depends on V, dtype and n_rows alone.
 constexpr int64_t kBlocks = 152;
 RuleCut rule_cut(int32_t V, int32_t most, int64_t n_rows) {
     constexpr int64_t kHead = 9;
