@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) process_rows_kernel(
     __syncthreads();
 
     if (wid >= kFirstProducer) {
-        rule_producer<DT, kNb, kRing>(
+        rule_producer<DT, kNb, kRing, true>(
             sm, p.r, cut, p.logits, p.ld_bytes, nullptr, p.r.n_rows, nullptr,
             [&](int s, int64_t r, int32_t slice) {
                 // out with the stage: whole vectors in bulk, ids after the last one by hand

@@ -66,10 +66,13 @@ struct __align__(16) RowDesc {
 constexpr int32_t kDescRebuild = 1, kDescMask = 2, kDescSparse = 4, kDescNew = 256;
 // Narrow masks: copied by vectors while they would take at most this part of the
 // slice.  (A copy of 16 bytes takes a memory sector of its own, and time to issue;
-// bulk copies of 16 bytes would take more, as a warp issues them one by one.)  Under 24
-// masks, wide and narrow: 8000 rows of 151936 bf16 scored take 1102 us if never, 950 up
-// to a fourth, 764 up to a sixteenth or a sixty-fourth; 1500 rows of 262144 with
-// entropy 254, 330, 281; 1000 rows of 151936 processed 158, 127, 115.
+// bulk copies of 16 bytes would take more, as a warp issues them one by one.)  1000 rows
+// of 151936 bf16 processed under masks that leave half of the ids and more, 2%, 0.1%, 32
+// ids: 125, 126, 118, 113 us up to a sixteenth, the same up to a sixty-fourth; 123, 152,
+// 119, 112 up to a fourth; 123, 123, 123, 122 if never.  Only ps_process_rows copies so: a row to
+// be scored is sooner in whole (8000 rows of 151936 under 24 masks of these kinds 530 us
+// and 735 with such copies, with 0.1% 425 and 725; 1500 rows of 262144 with entropy 228
+// and 269).
 constexpr int32_t kSparseShare = 16;
 constexpr int32_t kMade = 0x40000000;
 constexpr int32_t kFreshBad = 0x20000000;            // not an id of the vocabulary
@@ -222,11 +225,12 @@ struct RuleSpan {
     }
 };
 
-// A producer warp: fills stage `me` with every RING-th row.  Where a row's mask leaves few
-// of the slice's ids, only the 16-byte vectors that hold one are copied.
+// A producer warp: fills stage `me` with every RING-th row.
+// SPARSE: where a row's mask leaves few of the slice's ids, only the 16-byte vectors that
+// hold one are copied.
 // done(row, slice): called once the consumers have finished the stage's row, before
 // the stage is filled again.
-template <int DT, int NB, int RING, typename Done>
+template <int DT, int NB, int RING, bool SPARSE, typename Done>
 __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const RulesParams &p,
                                               const RuleCut &cut, const uint8_t *logits,
                                               int64_t ld_bytes,
@@ -299,21 +303,21 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
         }
         r_before = r;
         slice_before = map.slice;
-        // Logits and mask.  A mask that is not known yet is read word by word, behind
-        // the copy of all logits; the next time its size says how to copy.
+        // Logits and mask.  With SPARSE a mask that is not known yet is read word by word,
+        // behind the copy of all logits; the next time its size says how to copy.
         const uint32_t bytes = (uint32_t)(map.nid * kEsz + 15) / 16 * 16;
         const uint8_t *from = logits + src * ld_bytes;
         const bool masked = flags & kDescMask;
         const uint32_t *mrow = u.mask + (masked ? rm * u.mask_ld : 0);
         const uint64_t key = (uint64_t)(rm * cut.n_slices + map.slice) + 1;
         bool known = false;
-        if (masked) {
+        if (SPARSE && masked) {
             const uint64_t x = *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache];
             known = x >> 16 == key;
             if (known && (int32_t)(x & 0xffffu) * 16 * kSparseShare <= (int32_t)bytes) flags |= kDescSparse;
         }
         const bool sparse = flags & kDescSparse;
-        const bool copy_mask = masked && mask16 && !sparse && known;    // in bulk too
+        const bool copy_mask = masked && mask16 && !sparse && (known || !SPARSE);   // in bulk too
         if (!sparse) {
             if (lane == 0) {
                 fence_proxy_async_smem();
@@ -355,11 +359,11 @@ __device__ __forceinline__ void rule_producer(RuleSmem<DT, NB, RING> &sm, const 
                     make_uint4(m[i], m[i + 1], m[i + 2], m[i + 3]);
                 ids += __popc(m[i]) + __popc(m[i + 1]) + __popc(m[i + 2]) + __popc(m[i + 3]);
             }
-            if (!known) {
+            if (SPARSE && !known) {
                 ids = __reduce_add_sync(0xffffffffu, ids);
                 if (lane == 0) *(volatile uint64_t *)&sm.mask_ids[rm % kMaskCache] = key << 16 | ids;
             }
-            if (sparse) {
+            if (SPARSE && sparse) {
                 fence_proxy_async_smem();
 #pragma unroll
                 for (int i = 0; i < kWpl; ++i) {

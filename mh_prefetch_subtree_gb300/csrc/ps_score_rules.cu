@@ -14,8 +14,8 @@
 //
 // Where a mask leaves a lane at most kFewIds of its 64 (32 for float32) ids, the
 // warp steps through the allowed ones instead of exponentiating all (8000 rows of
-// 151936 bf16 under 24 masks: 764 us, never 824, up to 20 768; 1500 rows of 262144 with
-// entropy 281, 309, 282); where it leaves few of the slice, only their vectors are read from memory.
+// 151936 bf16 under 24 masks: 543 us, never 662, up to 20 542; 1500 rows of 262144 with
+// entropy 237, 296, 237; under masks that leave 0.1% of the ids 426, 625, 425 and 190, 285, 191).
 //
 // The reference only has to keep the exponentials in range, so without entropy
 // the warp keeps the one of the row before and looks for its ids' maximum only when
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
     __syncthreads();
 
     if (wid >= kFirstProducer) {
-        rule_producer<DT, kNb, kRing>(sm, p.r, p.cut, p.rows.logits, p.rows.ld_bytes,
+        rule_producer<DT, kNb, kRing, false>(sm, p.r, p.cut, p.rows.logits, p.rows.ld_bytes,
                                             p.rows.row_index, p.rows.n_logit_rows,
                                             p.rows.tokens, [](int, int64_t, int32_t) {});
         return;
@@ -540,9 +540,9 @@ cudaError_t launch_np(const ScoreRulesParams &p, int sms, cudaStream_t stream) {
 
 // As few slices as hold the vocabulary, or where there are few rows as many as
 // give every SM a block (of 1024 ids at least).  Segments of a slice (8000 rows of 151936
-// bf16 without masks, 150 rows of 50021 float32 with long histories): none 764 and 109 us,
-// 2: 626 and 78, 9: 599 and 68, all: 611 and 65, but with masks, whose segments are
-// copied too, 9: 765 and all: 800.
+// bf16 scored without masks and under 24, 150 rows of 50021 float32 with long histories
+// processed): none 775, 535 and 115 us, 2: 637, 533 and 86, 9: 608, 546 and 78, all: 614,
+// 607 and 76.
 // The blocks to cut for are a constant, and not the device's own multiprocessors (152 on a
 // GB300), so that a workspace's size depends on V, dtype and n_rows alone.
 constexpr int64_t kBlocks = 152;
