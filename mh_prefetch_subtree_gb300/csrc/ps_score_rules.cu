@@ -218,7 +218,7 @@ __device__ __forceinline__ void patch_rows(Smem &sm, const ScoreRulesParams &p) 
         }
         uint8_t *buf = sm.stage[s];
         const int4 dh = *reinterpret_cast<const int4 *>(&sm.desc[s]);       // tok, bad, flags, len
-        if ((dh.z & ~(kDescMask | kDescSparse)) && !walk.enter_row(s, dh.z, dh.w)) {
+        if ((dh.z & ~kDescMask) && !walk.enter_row(s, dh.z, dh.w)) {
             if (lane == 0) set_status(p.r.status, PS_DEV_TIMEOUT);
             return;
         }
