@@ -24,9 +24,11 @@
 // spread over the four lanes of a quad as one product needs them, so the quad
 // first exchanges words.
 //
-// What bounds it: 8 weights take 9 instructions to unpack, 5 of them on the integer
-// pipe, which takes one every other cycle; a multiprocessor gets 1 KB of weights
-// every 43 cycles from memory.
+// What bounds it: memory brings a multiprocessor 1 KB of weights every 43 cycles.
+// The integer pipe, which takes one instruction every other cycle, is at work 68% of the
+// time (1 row of 151936 x 4096, 68 us); unpacking, 5 integer instructions of 9 for
+// 8 weights, is less than half of that, and the rest is addresses (clamped for each
+// load), scale and zero words, and group indices.
 #include "ps_head.cuh"
 
 namespace ps {
@@ -421,7 +423,8 @@ cudaError_t launch(const HeadParams &p, int sms, cudaStream_t stream) {
 }
 
 // Hidden rows of a block: 8, 16 or 32, as many as there are and as fit.  With 8, a
-// warp takes 32 vocabulary rows (1 row of 151936 x 4096: 68 us, with 16: 96); with more
+// warp takes 32 vocabulary rows (1 row of 151936 x 4096: 68 us, with 16: 96), but 16 with
+// groups of 32 (119 us, with 32: 124; 262144 x 2048: 105, 128); with more
 // there are not the registers (16 rows: 105 us with 32, 92 with 16).  12 warps instead of
 // 16 pay with 32 hidden rows only (64 rows of 262144 x 2048: 254 and 279 us; 8 warps 274).
 template <int U, typename ScaleT>

@@ -23,6 +23,11 @@ struct HeadParams {
 __device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
 __device__ __forceinline__ __half2 h2_of(uint32_t x) { return *reinterpret_cast<__half2 *>(&x); }
 
+// A small integer put into the low bits of a float's mantissa and the power of two that
+// those bits then stand on taken off again, which is an old way to convert without a
+// conversion; for 4-bit weights and float16 it is in Kim, Henry, Fahim and Hassan Awadalla,
+// "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale
+// Production" (2022).
 // The four pairs (j, j + 4) of a word less the zero, as float16.  z1 holds
 // -(1024 + zero) twice, z16 -(64 + zero).
 __device__ __forceinline__ void unpack(uint32_t word, uint32_t z1, uint32_t z16, uint32_t (&x)[4]) {

@@ -688,14 +688,19 @@ cudaError_t launch_u(const HeadParams &p, int sms, cudaStream_t stream) {
 }  // namespace
 
 // Where both run, in us, this kernel and that of ps_head.cu:
-//   33 to 64 rows, 262144 x 2048, groups of 32, 64, 128: 321 / 328, 189 / 255, 144 / 230
+//   33 to 64 rows, 262144 x 2048, groups of 32, 64, 128: 308 / 336, 187 / 255, 144 / 230
 //                  65536 x 3968:                        266 / 412, 177 / 371, 130 / 349
-//   17 to 32 rows, 262144 x 2048:                        219 / 175, 154 / 136, 112 / 122
-//                  151936 x 4096:                        259 / 252, 175 / 199, 130 / 171
-//                  151936 x 1024:                         73 / 113, 54 / 103, 42 / 97
-// so groups of 32 are left to the other but for 64 rows at a time.  With fewer
-// vocabulary rows than fill all pipelines once it is the longer way of a unit that
-// counts: 64 rows of 2000 x 4096 and groups of 128 take 48 / 23, of 20000 x 2048 42 / 44.
+//   17 to 32 rows, 262144 x 2048:                        219 / 175, 152 / 140, 115 / 126
+//                  151936 x 4096:                        259 / 252, 179 / 201, 130 / 171
+//                  151936 x 1024:                         73 / 113, 57 / 109, 42 / 97
+// so groups of 32 are left to the other but for 64 rows at a time.  Groups of 64 and up to
+// 32 rows go either way: at 65536 and 151936 vocabulary rows this one takes 0.4 to 0.9 of the
+// other's time (32 rows, K from 512 to 3200), at 262144, where the other's rounds come out
+// even, it takes as long up to K = 1536 and 1.09 times as long above.  That is left so: a
+// rule by the other's rounds would follow single sizes.  With few vocabulary rows
+// it is the longer way of a unit that counts: 64 rows of 2000 x 4096 and groups of 128 take
+// 48 / 23, of 20000 x 2048 42 / 44, 32 rows of 40000 x 512, 1024, 2048 and groups of 64
+// 25 / 29, 37 / 38, 56 / 48, so a vocabulary has to fill all pipelines once.
 bool head_tile_takes(const HeadParams &p, int sms) {
     const Shape s = shape_of(p);
     return p.n_rows > 16 && p.head.K >= kStepK && s.rows > 0 && (p.head.group > 32 || s.rows == 64) &&
