@@ -529,6 +529,9 @@ ps_status ps_selftest_read(const void *data, size_t bytes, uint32_t *sink, void 
  * row_len       [n_rows], or NULL: a row sees its whole sequence.
  * row_mask      [n_rows]: the row's mask, or -1 for none; NULL: row r has mask r.
  *
+ * The struct is read during the call and its arrays by the kernels: a caller may
+ * keep one and write new tokens, lengths and masks into the arrays between calls.
+ *
  * What only the device can see sets bits in the status word, and the row's
  * results are NaN: PS_DEV_BAD_TOKEN for a history token outside [0, V);
  * PS_DEV_BAD_RULES for row_seq, row_len, row_mask, seq_begin or bias_begin out of
