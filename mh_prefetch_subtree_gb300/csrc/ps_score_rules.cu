@@ -14,7 +14,7 @@
 //
 // Where a mask leaves a lane at most kFewIds of its 64 (32 for float32) ids, the
 // warp steps through the allowed ones instead of exponentiating all (8000 rows of
-// 151936 bf16 under 24 masks: 543 us, never 662, up to 20 542; 1500 rows of 262144 with
+// 151936 bf16 under 24 masks: 543 us by events around one pass, never 662, up to 20 542; 1500 of 262144 with
 // entropy 237, 296, 237; under masks that leave 0.1% of the ids 426, 625, 425 and 190, 285, 191).
 //
 // The reference only has to keep the exponentials in range, so without entropy
@@ -458,6 +458,37 @@ __global__ void __launch_bounds__(rule_threads<kRing>(), 1) score_rules_kernel(
     }
 }
 
+// Part `a` relative to reference M >= a.R, and two parts as one.  References of parts with
+// like mass can be 124 / g apart, so a factor 2^(g d) alone may be below float32's range
+// where the sum times it is not (up to a fourth of a row's mass was lost so): it is applied
+// in two halves.
+template <int NP, bool ENT>
+__device__ __forceinline__ Acc moved(Acc a, float M, float g) {
+    if (a.R != -INFINITY) {
+        const float d = a.R - M, f = ex2(0.5f * d);
+        if constexpr (ENT) a.y1 = fmaf(d, a.s1, a.y1) * f * f;
+        a.s1 = a.s1 * f * f;
+        if constexpr (NP != 1) {
+            const float t = ex2(0.5f * d * (NP == 0 ? g : (float)NP));
+            a.st[0] = a.st[0] * t * t;
+        }
+    }
+    a.R = M;
+    return a;
+}
+template <int NP, bool ENT>
+__device__ __forceinline__ Acc joined(Acc a, Acc b, float g) {
+    const float M = fmaxf(a.R, b.R);
+    if (M != -INFINITY) {
+        a = moved<NP, ENT>(a, M, g);
+        b = moved<NP, ENT>(b, M, g);
+    }
+    a.s1 += b.s1;
+    if constexpr (NP != 1) a.st[0] += b.st[0];
+    if constexpr (ENT) a.y1 += b.y1;
+    return a;
+}
+
 // A row's parts, joined in their order by one warp; the result is in all lanes.
 // FAR: parts whose exponentials are 0 next to those of the row's largest logit, under tau
 // as well, are left out.
@@ -476,9 +507,18 @@ __device__ __forceinline__ Acc join_parts(const ChunkPart *parts, int n, float t
     for (int i = lane; i < n; i += 32) {
         const float4 s = __ldcg(reinterpret_cast<const float4 *>(parts + i));
         if (FAR && s.x < least) continue;
-        a = merge_part<NP, ENT>(a, Acc{s.x, s.y, {s.z, 0.f, 0.f}, s.w}, g);
+        a = joined<NP, ENT>(a, Acc{s.x, s.y, {s.z, 0.f, 0.f}, s.w}, g);
     }
-    return warp_merge<NP, ENT>(a, g);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Acc b = acc_empty();
+        b.R = __shfl_xor_sync(0xffffffffu, a.R, o);
+        b.s1 = __shfl_xor_sync(0xffffffffu, a.s1, o);
+        if constexpr (NP != 1) b.st[0] = __shfl_xor_sync(0xffffffffu, a.st[0], o);
+        if constexpr (ENT) b.y1 = __shfl_xor_sync(0xffffffffu, a.y1, o);
+        a = joined<NP, ENT>(a, b, g);
+    }
+    return a;
 }
 
 // One warp a row: its partial sums joined, then the results.  A part of logits like -1e12
