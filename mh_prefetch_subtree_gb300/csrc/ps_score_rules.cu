@@ -13,9 +13,10 @@
 // row, which a second kernel joins in their order.
 //
 // Where a mask leaves a lane at most kFewIds of its 64 (32 for float32) ids, the
-// warp steps through the allowed ones instead of exponentiating all (8000 rows of
-// 151936 bf16 under 24 masks: 543 us by events around one pass, never 662, up to 20 542; 1500 of 262144 with
-// entropy 237, 296, 237; under masks that leave 0.1% of the ids 426, 625, 425 and 190, 285, 191).
+// warp steps through the allowed ones instead of exponentiating all (events around one
+// pass: 8000 rows of 151936 bf16 under 24 masks 543 us, never 662, up to 20 542; 1500 rows
+// of 262144 with entropy 237, 296, 237; under masks that leave 0.1% of the ids 426, 625, 425
+// and 190, 285, 191).
 //
 // The reference only has to keep the exponentials in range, so without entropy
 // the warp keeps the one of the row before and looks for its ids' maximum only when
