@@ -260,8 +260,8 @@ __device__ __forceinline__ float bin_ref(float l, const Scale &s) {
     return __int_as_float(r);
 }
 // w relative to the reference's by 28 bits, rounded down, to be added up in two limbs of 14:
-// the 2^18 elements that a part of a row has at most add up to less than 2^32.  l - ref is
-// exact, or next to zero as good as.
+// the 2^18 elements that a part of a row has at most add up to less than 2^32 (the parts of a
+// cluster's blocks do not, and are added up in 64 bits).  l - ref is exact, or next to zero as good as.
 __device__ __forceinline__ uint32_t limbs(float l, float ref, const Scale &s, const uint64_t *table) {
     const float d = l - ref, h = d * s.gh;
     const uint64_t w = pow2_fixed(h, fmaf(d, s.gh, -h) + d * s.gl, 30, table);
@@ -326,7 +326,7 @@ struct Row {
     static constexpr int kT = kHalf ? 256 : 512, kResident = kHalf ? 5 : 2;
     static constexpr int kWarps = kT / 32, kBinsThread = kBins / kT;
     Shared &sh;
-    uint32_t *limb;              // float32: [2][kBins]
+    uint32_t *limb;              // float32: [2][kBins], a bin's sum of weights in two limbs
     const uint4 *vecs;
     int32_t V, n_vecs, id0;      // of the part; id of its first element
     uint32_t rank, blocks;
@@ -816,6 +816,11 @@ struct Order : Row<ElemT, ENT> {
     Before o;
     bool linear;                 // the bins are a second pass's
 
+    // What the limbs of a bin stand for.  A block's own (limbs()) are of 14 bits an element; the sum over
+    // a cluster's blocks has up to 48 bits, 2^20 elements of 28, and is held in limbs of 24.
+    __device__ __forceinline__ uint64_t limbs_sum(uint32_t hi, uint32_t low) const {
+        return ((uint64_t)hi << (blocks > 1 ? 24 : 14)) + low;
+    }
     // A bin's mass, and its elements; none where it lies below what min-p leaves.
     __device__ __forceinline__ uint64_t bin_mass(int bin, uint32_t *n) const {
         const int at = bin_slot(bin, linear);
@@ -829,7 +834,7 @@ struct Order : Row<ElemT, ENT> {
         if (!(h > -(float)s.bits - 2.f) || *n == 0) return 0;
         const uint64_t w = pow2_fixed(h, e, s.bits, sh.pow);
         if (one) return w * *n;
-        const uint64_t part = kHalf ? sh.near0_all : ((uint64_t)limb[at] << 14) + limb[kBins + at];
+        const uint64_t part = kHalf ? sh.near0_all : limbs_sum(limb[at], limb[kBins + at]);
         return __umul64hi(w, part) << 36 | w * part >> 28;
     }
     __device__ __forceinline__ void order(const Command &c) {
@@ -864,21 +869,31 @@ struct Order : Row<ElemT, ENT> {
     // The bins of all blocks.
     __device__ __forceinline__ void add_up() {
         // the loads of all blocks are under way together
-        auto add = [&](uint32_t *bins, int n) {
+        if (blocks > 1) {
 #pragma unroll 1
-            for (int i = threadIdx.x * 4; i < n; i += kT * 4) {
+            for (int i = threadIdx.x * 4; i < kBins; i += kT * 4) {
                 uint4 t = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
                 for (uint32_t b = 0; b < blocks; ++b) {
-                    const uint4 v = get4(at_block(bins + i, b));
+                    const uint4 v = get4(at_block(sh.bins + i, b));
                     t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
                 }
-                *reinterpret_cast<uint4 *>(bins + i) = t;
+                *reinterpret_cast<uint4 *>(sh.bins + i) = t;
             }
-        };
-        if (blocks > 1) {
-            add(sh.bins, kBins);
-            if constexpr (!kHalf) add(limb, 2 * kBins);
+            if constexpr (!kHalf) {
+#pragma unroll 1
+                for (int i = threadIdx.x * 4; i < kBins; i += kT * 4) {
+                    uint64_t t[4] = {};
+#pragma unroll 4
+                    for (uint32_t b = 0; b < blocks; ++b) {
+                        const uint4 h = get4(at_block(limb + i, b)), l = get4(at_block(limb + kBins + i, b));
+                        t[0] += ((uint64_t)h.x << 14) + l.x, t[1] += ((uint64_t)h.y << 14) + l.y;
+                        t[2] += ((uint64_t)h.z << 14) + l.z, t[3] += ((uint64_t)h.w << 14) + l.w;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) limb[i + q] = (uint32_t)(t[q] >> 24), limb[kBins + i + q] = (uint32_t)t[q] & 0xffffffu;
+                }
+            }
         }
         if (kHalf && threadIdx.x < 32) {
             uint64_t part = 0;
