@@ -1052,7 +1052,8 @@ struct Order : Row<ElemT, ENT> {
         const uint32_t left = r.equal;
         uint32_t j = c;
         if (c == 0) {
-            j = w ? (uint32_t)fminf(__fdividef((float)t, (float)w), (float)left) : 1;
+            // without a mass (see settle()) the last
+            j = w ? (uint32_t)fminf(__fdividef((float)t, (float)w), (float)left) : left;
             j = max(min(j, left), 1u);
             while (j > 1 && (j - 1) * w >= t) --j;
             while (j < left && j * w < t) ++j;
@@ -1128,8 +1129,11 @@ struct Order : Row<ElemT, ENT> {
                 if (x.x > me.x || same) b += xw, ++nb;
                 nth += same, equal += x.x == me.x;
             }
+            // t may be more than the elements' masses, each rounded by itself, add up to.  Where all
+            // of them round to none, the bin has its mass at its last element, as the prefix that
+            // ends with the bin is then the first to hold t.
             const uint64_t to = min(t, all);
-            if (number ? nb + 1 == c : b < to && b + w >= to) {
+            if (number ? nb + 1 == c : all == 0 ? nb + 1 == len : b < to && b + w >= to) {
                 Result q;
                 q.before = r.before + b;
                 q.count = r.count + nb;
