@@ -113,7 +113,8 @@ struct Shared {
     uint32_t scan_n[kMostWarps], scan_k[kMostWarps];
     float scan_f[2][kMostWarps];
     float lnp[2];                                 // tau ln(min_p), as two floats
-    uint32_t near0[2];                            // bfloat16: the limbs of the bin around zero
+    // bfloat16: the limbs of the bin around zero; its sums of e^l and l log2 e e^l for log p0, by 23 and 28 bits
+    uint32_t near0[4];
     // written by the cluster's blocks, read by the first
     Part part[kMostBlocks];
     uint64_t mass[kMostBlocks];
@@ -121,6 +122,7 @@ struct Shared {
     Command cmd;
     // the first block's
     uint64_t near0_all;
+    float near0_sum, near0_ent;
     uint32_t n_list;                              // in the first pass every block's: values around zero
     int at;
     Result res;
@@ -505,7 +507,7 @@ struct Row {
             z = reinterpret_cast<uint4 *>(limb);
             for (int i = threadIdx.x; i < 2 * kBins / 4; i += kT) z[i] = make_uint4(0, 0, 0, 0);
         }
-        if (threadIdx.x < 2) sh.near0[threadIdx.x] = 0;
+        if (threadIdx.x < 4) sh.near0[threadIdx.x] = 0;
         if (threadIdx.x == 0) sh.n_list = 0;
     }
     // Sums over the block, to the first block.
@@ -569,6 +571,12 @@ struct Row {
                 const uint32_t m = limbs(x, bin_ref(x, s), s, sh.pow);
                 atomicAdd(&sh.near0[0], m >> 14);
                 atomicAdd(&sh.near0[1], m & 16383u);
+                // e^l by its series: |l| < 2^-7.9, the next term is below 2^-36.  256 of them fit, and
+                // integers do not depend on the list's order.  (Where tau > 4, |l| is larger and a second
+                // pass does this.)
+                const float e = x * fmaf(x, fmaf(x, 0.16666667f, 0.5f), 1.f);      // - 1
+                atomicAdd(&sh.near0[2], 0x800000u + (uint32_t)__float2int_rn(e * 0x1p23f));
+                if (ENT) atomicAdd(&sh.near0[3], (uint32_t)__float2int_rn(x * kLog2e * (1.f + e) * 0x1p28f));
             }
             // M: of the first bin that is not empty, if that is a value's own and the others are whole
             uint32_t first = kBins;
@@ -897,10 +905,17 @@ struct Order : Row<ElemT, ENT> {
         }
         if (kHalf && threadIdx.x < 32) {
             uint64_t part = 0;
-            if (threadIdx.x < blocks)
-                part = ((uint64_t)get(at_block(&sh.near0[0], threadIdx.x)) << 14) + get(at_block(&sh.near0[1], threadIdx.x));
+            float sum = 0.f, ent = 0.f;
+            if (threadIdx.x < blocks) {
+                const uint32_t a = at_block(&sh.near0[0], threadIdx.x);
+                part = ((uint64_t)get(a) << 14) + get(a + 4);
+                sum = (float)get(a + 8) * 0x1p-23f;
+                if (ENT) ent = (float)(int32_t)get(a + 12) * 0x1p-28f;
+            }
             part = warp_sum64(part);
-            if (threadIdx.x == 0) sh.near0_all = part;
+            sum = warp_sum(sum);
+            if (ENT) ent = warp_sum(ent);
+            if (threadIdx.x == 0) sh.near0_all = part, sh.near0_sum = sum, sh.near0_ent = ent;
         }
         __syncthreads();
         // around zero the first pass has two
@@ -915,7 +930,8 @@ struct Order : Row<ElemT, ENT> {
             __syncthreads();
         }
     }
-    // The running sums; of bfloat16 rows after a first pass also those of log p0, in `part`.
+    // The running sums; of bfloat16 rows after a first pass also those of log p0, in `part`, but for
+    // the bin around zero.
     __device__ __forceinline__ void sum_up(bool counts, Part *part) {
         const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
         o.m_here = 0, o.n_here = 0;
@@ -948,14 +964,6 @@ struct Order : Row<ElemT, ENT> {
                 uint32_t n;
                 o.m_here += bin_mass(s.top, &n);
                 o.n_here += n;
-                n = sh.bins[bin_slot(s.top, linear)];
-                if (counts && n) {
-                    // the value that has the mean mass
-                    const float l = bin_most(s.top, s) + __log2f((float)sh.near0_all / ((float)n * 0x1p28f)) / s.gh;
-                    const float y = (l - s.M) * kLog2e, x = (float)n * ex2(y);
-                    sum += x;
-                    if (ENT) ent = fmaf(x, y, ent);
-                }
             }
         } else {
 #pragma unroll 1
@@ -1297,8 +1305,10 @@ __global__ void __launch_bounds__(Row<ElemT, ENT>::kT, Row<ElemT, ENT>::kResiden
     x.linear = again;
     x.add_up();
     x.sum_up(!again, &all);
+    // e^-M, where sums are of e^l
+    auto down_from = [](float M, float yh) { return ex2(-yh) * (1.f - kLn2f * (fmaf(M, kLog2e, -yh) + M * kLog2eLow)); };
     if (!kHalf || again) {
-        const float yh = M * kLog2e, down = again ? 1.f : ex2(-yh) * (1.f - kLn2f * (fmaf(M, kLog2e, -yh) + M * kLog2eLow));
+        const float yh = M * kLog2e, down = again ? 1.f : down_from(M, yh);
         for (uint32_t b = 0; b < blocks; ++b) {
             const Part q = sh.part[b];
             const float to = again ? 0.f : yh;
@@ -1413,6 +1423,12 @@ __global__ void __launch_bounds__(Row<ElemT, ENT>::kT, Row<ElemT, ENT>::kResiden
         p.lq[row] = lq;
     }
     if (tid == 32 && (p.lp0 || ENT)) {
+        if (kHalf && !x.linear) {
+            // what lies around zero: M is not among it
+            const float yh = M * kLog2e, down = down_from(M, yh);
+            all.sum = fmaf(sh.near0_sum, down, all.sum);
+            if (ENT) all.ent = fmaf(fmaf(-yh, sh.near0_sum, sh.near0_ent), down, all.ent);
+        }
         // log of 1 and the rest: of a small rest to its own digits
         const float rest = (float)(all.maxima - 1) + all.sum;
         const double log_z = rest < 0.5f ? (double)log1pf(rest)
