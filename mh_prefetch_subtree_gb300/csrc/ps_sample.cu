@@ -20,9 +20,12 @@
 //
 // Masses are integers, 2^43 to 2^45 for a mass of 1, so their sums are exact and do not
 // depend on the order of the additions: the same row and number give the same token
-// however the row is divided.  w is formed from y in two floats to about 2^-31 of itself,
-// so that a token differs from that of a float64 evaluation only where u Z lies that close
-// to a border between two ids.
+// however the row is divided.  w is formed from y in two floats to about 2^-31 of itself, and
+// a bin of several values (float32 rows, values around zero) adds weights of 28 bits below
+// its largest value's: up to 2^-27 of an element at the lower end of a bin that is two units of y
+// wide, the widest.  A token differs from that of a float64 evaluation only where u Z lies that
+// close to a border between two ids.  Such a bin's mass and its elements', each rounded by
+// itself, are two roundings of one sum; what ends with the bin ends where its mass does.
 //
 // A row is one block's, or with few rows a cluster's: its blocks each read a part, and the
 // first adds up their bins.
@@ -261,13 +264,12 @@ __device__ __forceinline__ float bin_ref(float l, const Scale &s) {
     if ((int32_t)((uint32_t)(b & 0x7fffffff) >> s.shift) <= s.zero) r = (s.zero << s.shift) | mask;
     return __int_as_float(r);
 }
-// w relative to the reference's by 28 bits, rounded down, to be added up in two limbs of 14:
+// w relative to the reference's by 28 bits, to be added up in two limbs of 14:
 // the 2^18 elements that a part of a row has at most add up to less than 2^32 (the parts of a
 // cluster's blocks do not, and are added up in 64 bits).  l - ref is exact, or next to zero as good as.
 __device__ __forceinline__ uint32_t limbs(float l, float ref, const Scale &s, const uint64_t *table) {
     const float d = l - ref, h = d * s.gh;
-    const uint64_t w = pow2_fixed(h, fmaf(d, s.gh, -h) + d * s.gl, 30, table);
-    return min((uint32_t)(w >> 2), (1u << 28) - 1);
+    return min((uint32_t)pow2_fixed(h, fmaf(d, s.gh, -h) + d * s.gl, 28, table), (1u << 28) - 1);
 }
 
 // ln(m 2^-scale), m > 0, to about 2^-30: an estimate x and how far m e^-x is from 1.
