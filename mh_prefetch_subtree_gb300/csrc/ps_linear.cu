@@ -518,14 +518,30 @@ cudaError_t launch_n(const LinearParams &p, int sms, cudaStream_t stream) {
     return exact ? launch<N, 1, false, true>(p, 1, sms, stream) : launch<N, 1, false, false>(p, 1, sms, stream);
 }
 
-}  // namespace
-
-cudaError_t launch_linear(const LinearParams &p, int sms, cudaStream_t stream) {
+cudaError_t launch_rows(const LinearParams &p, int sms, cudaStream_t stream) {
     if (p.n_rows <= 16) return launch_n<16>(p, sms, stream);
     if (p.n_rows <= 32) return launch_n<32>(p, sms, stream);
     if (p.n_rows <= 64) return launch_n<64>(p, sms, stream);
     if (p.n_rows <= 128) return launch_n<128>(p, sms, stream);
     return launch_n<256>(p, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearParams &params, int sms, cudaStream_t stream) {
+    // The kernel counts rows, a tile's last ones among them, in 32 bits.
+    constexpr int64_t kMostRows = (int64_t)1 << 30;             // of a launch
+    const int64_t esz = params.dtype == PS_BF16 ? 2 : 4;
+    for (int64_t r = 0; r < params.n_rows; r += kMostRows) {
+        LinearParams p = params;
+        p.n_rows = (int32_t)std::min(params.n_rows - r, kMostRows);
+        p.x = (const uint8_t *)params.x + r * params.x_ld * 2;
+        p.out = (uint8_t *)params.out + r * params.ld * esz;
+        if (params.residual) p.residual = (const uint8_t *)params.residual + r * params.residual_ld * esz;
+        const cudaError_t e = launch_rows(p, sms, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace ps
