@@ -45,24 +45,25 @@ extern "C" {
 ps_status ps_linear_rows(const ps_linear *h, const void *x, int64_t x_ld, int32_t n_rows,
                          const void *residual, int64_t residual_ld, void *out, int64_t ld,
                          int32_t dtype, void *cuda_stream) {
-    constexpr int64_t kMostLd = int64_t(1) << 40;
+    // Elements that an array may span: more is no memory, and fewer are counted in bytes below.
+    constexpr int64_t kMostSpan = int64_t(1) << 40;
     if (!h || n_rows < 0 || h->N < 1 || h->K < 1 || h->K % 8 != 0) return PS_ERR_INVALID_ARG;
     const int esz = elem_size(dtype);
     if (esz == 0 || (h->bias && elem_size(h->bias_dtype) == 0)) return PS_ERR_UNSUPPORTED;
     if (h->act < PS_ACT_NONE || h->act > PS_ACT_GELU) return PS_ERR_UNSUPPORTED;
     if (h->act == PS_ACT_CAP && !(h->cap > 0.f && isfinite(h->cap))) return PS_ERR_INVALID_ARG;
-    if (!h->w || !aligned(h->w, 16) || h->w_ld < h->K || h->w_ld % 8 != 0 || h->w_ld > (int64_t(1) << 38) ||
+    if (!h->w || !aligned(h->w, 16) || h->w_ld < h->K || h->w_ld % 8 != 0 || h->w_ld > kMostSpan / h->N ||
         (h->bias && !aligned(h->bias, (size_t)elem_size(h->bias_dtype))))
         return PS_ERR_INVALID_ARG;
     if (n_rows == 0) return PS_OK;
-    if (!x || !aligned(x, 16) || x_ld < h->K || x_ld % 8 != 0 || x_ld > (int64_t(1) << 38)) return PS_ERR_INVALID_ARG;
+    if (!x || !aligned(x, 16) || x_ld < h->K || x_ld % 8 != 0 || x_ld > kMostSpan / n_rows) return PS_ERR_INVALID_ARG;
     ps_status st = check_rows_layout(out, h->N, dtype, ld);
     if (st != PS_OK) return st;
     if (residual) {
         st = check_rows_layout(residual, h->N, dtype, residual_ld);
         if (st != PS_OK) return st;
     }
-    if (ld > kMostLd / n_rows || (residual && residual_ld > kMostLd / n_rows)) return PS_ERR_INVALID_ARG;
+    if (ld > kMostSpan / n_rows || (residual && residual_ld > kMostSpan / n_rows)) return PS_ERR_INVALID_ARG;
     const int64_t n_out = ((n_rows - 1) * ld + h->N) * esz;
     if (overlap(out, n_out, x, ((n_rows - 1) * x_ld + h->K) * 2) ||
         overlap(out, n_out, h->w, ((h->N - 1) * h->w_ld + h->K) * 2) ||
