@@ -723,7 +723,7 @@ ps_status ps_score_rows_truncated(const ps_subtree_batch *batch, const ps_sampli
  * result is rounded once.  The order of the sums depends on the sizes, not on the values:
  * the same call gives the same bits.
  *
- * N, K         outputs and inputs of a row; K is a multiple of 8.
+ * N, K         outputs and inputs of a row; K is a multiple of 8, at most 2^24.
  * act          ps_act.  PS_ACT_CAP is cap tanh(z / cap), PS_ACT_SILU z / (1 + exp(-z)),
  *              PS_ACT_GELU z times the normal distribution function.
  * cap          > 0 and finite; read with PS_ACT_CAP.

@@ -47,7 +47,9 @@ ps_status ps_linear_rows(const ps_linear *h, const void *x, int64_t x_ld, int32_
                          int32_t dtype, void *cuda_stream) {
     // Elements that an array may span: more is no memory, and fewer are counted in bytes below.
     constexpr int64_t kMostSpan = int64_t(1) << 40;
-    if (!h || n_rows < 0 || h->N < 1 || h->K < 1 || h->K % 8 != 0) return PS_ERR_INVALID_ARG;
+    // A block waits for a whole tile's sums, up to 2^18 steps of its copies: a tenth of a second, far from a wait's 2.
+    constexpr int32_t kMostK = 1 << 24;
+    if (!h || n_rows < 0 || h->N < 1 || h->K < 1 || h->K > kMostK || h->K % 8 != 0) return PS_ERR_INVALID_ARG;
     const int esz = elem_size(dtype);
     if (esz == 0 || (h->bias && elem_size(h->bias_dtype) == 0)) return PS_ERR_UNSUPPORTED;
     if (h->act < PS_ACT_NONE || h->act > PS_ACT_GELU) return PS_ERR_UNSUPPORTED;
