@@ -726,7 +726,7 @@ ps_status ps_score_rows_truncated(const ps_subtree_batch *batch, const ps_sampli
  * N, K         outputs and inputs of a row; K is a multiple of 8, at most 2^24.
  * act          ps_act.  PS_ACT_CAP is cap tanh(z / cap), PS_ACT_SILU z / (1 + exp(-z)),
  *              PS_ACT_GELU z times the normal distribution function.
- * cap          > 0 and finite; read with PS_ACT_CAP.
+ * cap          2^-60 .. 2^60; read with PS_ACT_CAP.
  * bias_dtype   ps_dtype of bias.
  * w_ld         elements from a row of w to the next, a multiple of 8, >= K.
  * w            [N][w_ld] bfloat16, 16-byte aligned.

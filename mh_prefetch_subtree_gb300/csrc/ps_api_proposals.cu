@@ -1,7 +1,5 @@
 // Host side of the entry points around proposals: projections of hidden rows, and drawing
 // and scoring tokens under truncation.  See include/ps.h for the contract.
-#include <math.h>
-
 #include <initializer_list>
 
 #include "ps_api.cuh"
@@ -53,7 +51,8 @@ ps_status ps_linear_rows(const ps_linear *h, const void *x, int64_t x_ld, int32_
     const int esz = elem_size(dtype);
     if (esz == 0 || (h->bias && elem_size(h->bias_dtype) == 0)) return PS_ERR_UNSUPPORTED;
     if (h->act < PS_ACT_NONE || h->act > PS_ACT_GELU) return PS_ERR_UNSUPPORTED;
-    if (h->act == PS_ACT_CAP && !(h->cap > 0.f && isfinite(h->cap))) return PS_ERR_INVALID_ARG;
+    // the kernel multiplies by 1 / cap, which is to be far from what float32 cannot hold
+    if (h->act == PS_ACT_CAP && !(h->cap >= 0x1p-60f && h->cap <= 0x1p60f)) return PS_ERR_INVALID_ARG;
     if (!h->w || !aligned(h->w, 16) || h->w_ld < h->K || h->w_ld % 8 != 0 || h->w_ld > kMostSpan / h->N ||
         (h->bias && !aligned(h->bias, (size_t)elem_size(h->bias_dtype))))
         return PS_ERR_INVALID_ARG;
