@@ -1,5 +1,6 @@
 // Host side of the entry points around proposals: projections of hidden rows, and drawing
 // and scoring tokens under truncation.  See include/ps.h for the contract.
+#include <algorithm>
 #include <initializer_list>
 
 #include "ps_api.cuh"
@@ -43,8 +44,9 @@ extern "C" {
 ps_status ps_linear_rows(const ps_linear *h, const void *x, int64_t x_ld, int32_t n_rows,
                          const void *residual, int64_t residual_ld, void *out, int64_t ld,
                          int32_t dtype, void *cuda_stream) {
-    // Elements that an array may span: more is no memory, and fewer are counted in bytes below.
-    constexpr int64_t kMostSpan = int64_t(1) << 40;
+    // Elements that an array may span: more is no memory, and fewer are counted in bytes below.  A
+    // copied tile's rows are at most 2^39 bytes apart.
+    constexpr int64_t kMostSpan = int64_t(1) << 40, kMostStride = int64_t(1) << 38;
     // A block waits for a whole tile's sums, up to 2^18 steps of its copies: a tenth of a second, far from a wait's 2.
     constexpr int32_t kMostK = 1 << 24;
     if (!h || n_rows < 0 || h->N < 1 || h->K < 1 || h->K > kMostK || h->K % 8 != 0) return PS_ERR_INVALID_ARG;
@@ -53,11 +55,11 @@ ps_status ps_linear_rows(const ps_linear *h, const void *x, int64_t x_ld, int32_
     if (h->act < PS_ACT_NONE || h->act > PS_ACT_GELU) return PS_ERR_UNSUPPORTED;
     // the kernel multiplies by 1 / cap, which is to be far from what float32 cannot hold
     if (h->act == PS_ACT_CAP && !(h->cap >= 0x1p-60f && h->cap <= 0x1p60f)) return PS_ERR_INVALID_ARG;
-    if (!h->w || !aligned(h->w, 16) || h->w_ld < h->K || h->w_ld % 8 != 0 || h->w_ld > kMostSpan / h->N ||
+    if (!h->w || !aligned(h->w, 16) || h->w_ld < h->K || h->w_ld % 8 != 0 || h->w_ld > std::min(kMostSpan / h->N, kMostStride) ||
         (h->bias && !aligned(h->bias, (size_t)elem_size(h->bias_dtype))))
         return PS_ERR_INVALID_ARG;
     if (n_rows == 0) return PS_OK;
-    if (!x || !aligned(x, 16) || x_ld < h->K || x_ld % 8 != 0 || x_ld > kMostSpan / n_rows) return PS_ERR_INVALID_ARG;
+    if (!x || !aligned(x, 16) || x_ld < h->K || x_ld % 8 != 0 || x_ld > std::min(kMostSpan / n_rows, kMostStride)) return PS_ERR_INVALID_ARG;
     ps_status st = check_rows_layout(out, h->N, dtype, ld);
     if (st != PS_OK) return st;
     if (residual) {

@@ -21,6 +21,7 @@ def built():
     (3, 8, 2 ** 29, 2 ** 12, 2 ** 29),
     (0, 8, 2 ** 27, 2 ** 38, 2 ** 27),          # before any row is asked for
     (2 ** 31 - 1, 8, 8, 8, 2 ** 30),            # out
+    (0, 8, 1, 2 ** 39, 8),                      # a row, and the next one further than a tile's rows may be
 ])
 def test_spans(rows, x_ld, w_rows, w_ld, ld):
     x, w, out = (torch.zeros(64, dtype=torch.bfloat16) for _ in range(3))
