@@ -104,7 +104,7 @@ ps_status ps_sample_rows(const ps_sampling *sampling, int32_t V, int32_t dtype, 
     st = check_rows_layout(logits, V, dtype, ld);
     if (st != PS_OK) return st;
     if (!u || !tokens || n_rows > (int64_t(1) << 62) / ld / esz) return PS_ERR_INVALID_ARG;
-    if (!aligned(u, 8) || !aligned(tokens, 4) || !aligned(lp0, 8) || !aligned(lq, 8) || !aligned(entropy, 8))
+    if (!aligned(u, 8) || !aligned(tokens, 4) || !aligned(lp0, 8) || !aligned(lq, 8) || !aligned(entropy, 8) || !aligned(status, 4))
         return PS_ERR_INVALID_ARG;
     if (!all_on_device({u, tokens, lp0, lq, entropy, status}) || !sampling_on_device(sampling)) return PS_ERR_INVALID_ARG;
     int sms = 0;
@@ -135,7 +135,9 @@ ps_status ps_score_rows_truncated(const ps_subtree_batch *b, const ps_sampling *
     if (!status || (b->n_rows > 0 && (!lp0 || !lq))) return PS_ERR_INVALID_ARG;
     st = check_sampling_host(sampling, b->V, b->n_rows);
     if (st != PS_OK || b->n_rows == 0) return st;
-    if (!aligned(lp0, 8) || !aligned(lq, 8) || !aligned(entropy, 8)) return PS_ERR_INVALID_ARG;
+    if (!aligned(b->tokens, 4) || !aligned(b->row_index, 8) || !aligned(lp0, 8) || !aligned(lq, 8) || !aligned(entropy, 8) ||
+        !aligned(status, 4))
+        return PS_ERR_INVALID_ARG;
     if (!all_on_device({b->tokens, b->row_index, lp0, lq, entropy, status}) || !sampling_on_device(sampling))
         return PS_ERR_INVALID_ARG;
     int sms = 0;
