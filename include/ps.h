@@ -758,6 +758,16 @@ ps_status ps_linear_rows(const ps_linear *linear, const void *x, int64_t x_ld, i
                          const void *residual, int64_t residual_ld, void *out, int64_t ld,
                          int32_t dtype, void *cuda_stream);
 
+/*
+ * Diagnostic, not a step of the method: ps_linear_rows by tiles of 64 rows of x (256 for more
+ * than 64 rows), whose first block leaves out its copies once its ring of at most 11 steps of
+ * 64 inputs has been filled, as if they never landed, and in which every wait gives up after
+ * 0.1 s.  Outputs are those of an undisturbed call or NaN, and NaN wherever copies were left out.
+ */
+ps_status ps_selftest_linear_wait(const ps_linear *linear, const void *x, int64_t x_ld,
+                                  int32_t n_rows, const void *residual, int64_t residual_ld,
+                                  void *out, int64_t ld, int32_t dtype, void *cuda_stream);
+
 /* Static text for a status code. */
 const char *ps_status_string(ps_status status);
 

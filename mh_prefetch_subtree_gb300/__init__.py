@@ -183,6 +183,8 @@ def lib() -> ctypes.CDLL:
         L.ps_linear_rows.argtypes = [ctypes.POINTER(PsLinear), _vp, ctypes.c_int64, ctypes.c_int32,
                                      _vp, ctypes.c_int64, _vp, ctypes.c_int64, ctypes.c_int32, _vp]
         L.ps_linear_rows.restype = ctypes.c_int
+        L.ps_selftest_linear_wait.argtypes = L.ps_linear_rows.argtypes
+        L.ps_selftest_linear_wait.restype = ctypes.c_int
         L.ps_sample_rows.argtypes = [ctypes.POINTER(PsSampling), ctypes.c_int32, ctypes.c_int32,
                                      ctypes.c_int64, _vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp,
                                      _vp, _vp]
@@ -389,11 +391,8 @@ def ps_score_rows_rules(batch: PsSubtreeBatch, rules: PsLogitRules, lp0: torch.T
     return st
 
 
-def ps_linear_rows(linear: PsLinear, x: torch.Tensor, out: torch.Tensor,
-                   residual: torch.Tensor | None = None, stream=None, check: bool = True) -> int:
-    """out[:, :N] = act(x W^T + bias) + residual (see include/ps.h): x is [n_rows, >= K]
-    bfloat16, out [n_rows, ld] bfloat16 or float32, residual None or of out's type; it may be
-    out itself."""
+def _linear_call(name: str, linear: PsLinear, x: torch.Tensor, out: torch.Tensor,
+                 residual: torch.Tensor | None, stream, check: bool) -> int:
     _need(x, torch.bfloat16, "x")
     dt = _row_dtype(out, "out")
     shape, out_shape = x.shape, out.shape
@@ -405,11 +404,25 @@ def ps_linear_rows(linear: PsLinear, x: torch.Tensor, out: torch.Tensor,
         if residual.dim() != 2 or residual.shape[0] != shape[0]:
             raise ValueError("residual must be a matrix with as many rows as out")
         res_ld = residual.shape[1]
-    st = (_lib or lib()).ps_linear_rows(linear, _ptr(x), shape[1], shape[0], _ptr(residual), res_ld,
-                                        _ptr(out), out_shape[1], dt, _stream(stream, out))
+    st = getattr(_lib or lib(), name)(linear, _ptr(x), shape[1], shape[0], _ptr(residual), res_ld,
+                                      _ptr(out), out_shape[1], dt, _stream(stream, out))
     if check and st != PS_OK:
-        raise PsError(st, "ps_linear_rows")
+        raise PsError(st, name)
     return st
+
+
+def ps_linear_rows(linear: PsLinear, x: torch.Tensor, out: torch.Tensor,
+                   residual: torch.Tensor | None = None, stream=None, check: bool = True) -> int:
+    """out[:, :N] = act(x W^T + bias) + residual (see include/ps.h): x is [n_rows, >= K]
+    bfloat16, out [n_rows, ld] bfloat16 or float32, residual None or of out's type; it may be
+    out itself."""
+    return _linear_call("ps_linear_rows", linear, x, out, residual, stream, check)
+
+
+def ps_selftest_linear_wait(linear: PsLinear, x: torch.Tensor, out: torch.Tensor,
+                            residual: torch.Tensor | None = None, stream=None, check: bool = True) -> int:
+    """Diagnostic: ps_linear_rows with copies left out and short waits (see include/ps.h)."""
+    return _linear_call("ps_selftest_linear_wait", linear, x, out, residual, stream, check)
 
 
 def ps_sample_rows(sampling: PsSampling, logits: torch.Tensor, u: torch.Tensor,

@@ -37,13 +37,9 @@ bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
     return x < y + nb && y < x + na;
 }
 
-}  // namespace
-
-extern "C" {
-
-ps_status ps_linear_rows(const ps_linear *h, const void *x, int64_t x_ld, int32_t n_rows,
-                         const void *residual, int64_t residual_ld, void *out, int64_t ld,
-                         int32_t dtype, void *cuda_stream) {
+// Checks a projection's arguments and launches it.
+ps_status linear_rows(const ps_linear *h, const void *x, int64_t x_ld, int32_t n_rows, const void *residual,
+                      int64_t residual_ld, void *out, int64_t ld, int32_t dtype, bool lost, void *cuda_stream) {
     // Elements that an array may span: more is no memory, and fewer are counted in bytes below.  A
     // copied tile's rows are at most 2^39 bytes apart.
     constexpr int64_t kMostSpan = int64_t(1) << 40, kMostStride = int64_t(1) << 38;
@@ -89,7 +85,23 @@ ps_status ps_linear_rows(const ps_linear *h, const void *x, int64_t x_ld, int32_
     p.residual_ld = residual_ld;
     p.out = out;
     p.ld = ld;
-    return map_cuda(launch_linear(p, sms, (cudaStream_t)cuda_stream));
+    return map_cuda(launch_linear(p, sms, lost, (cudaStream_t)cuda_stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+ps_status ps_linear_rows(const ps_linear *linear, const void *x, int64_t x_ld, int32_t n_rows,
+                         const void *residual, int64_t residual_ld, void *out, int64_t ld,
+                         int32_t dtype, void *cuda_stream) {
+    return linear_rows(linear, x, x_ld, n_rows, residual, residual_ld, out, ld, dtype, false, cuda_stream);
+}
+
+ps_status ps_selftest_linear_wait(const ps_linear *linear, const void *x, int64_t x_ld, int32_t n_rows,
+                                  const void *residual, int64_t residual_ld, void *out, int64_t ld,
+                                  int32_t dtype, void *cuda_stream) {
+    return linear_rows(linear, x, x_ld, n_rows, residual, residual_ld, out, ld, dtype, true, cuda_stream);
 }
 
 ps_status ps_sample_rows(const ps_sampling *sampling, int32_t V, int32_t dtype, int64_t n_rows,

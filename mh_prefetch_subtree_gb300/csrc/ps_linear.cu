@@ -42,6 +42,7 @@ template <int N>
 constexpr int kExactSteps = N == 256 ? 8 : 2;
 constexpr int kMostRing = 11, kMostSplit = 8;
 constexpr int kSmem = 226 * 1024;
+constexpr uint64_t kTestWaitNs = 100000000ull;                // in the diagnostic variant
 
 struct Bars {
     uint64_t full[kMostRing], empty[kMostRing];
@@ -189,7 +190,8 @@ __device__ __forceinline__ void put_out(const LinearParams &p, int64_t r, int v,
 }
 
 // EXACT: sums of kExact steps are added up in registers, for float32 outputs and divided k.
-template <int N, int C, bool SPLIT, bool EXACT>
+// LOST (the diagnostic variant): the first block brings no copies once its ring has been filled.
+template <int N, int C, bool SPLIT, bool EXACT, bool LOST>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const LinearParams p, const int n_ring, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x) {
     constexpr int kBytesX = N / C * kStep * 2, kSlot = kBytesW + kBytesX;
@@ -197,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(EXACT || !SPLIT, "a divided k's sums are in registers");
     constexpr uint32_t kCols = 2 * N < 32 ? 32 : 2 * N;
     constexpr int kExact = kExactSteps<N>;
+    constexpr uint64_t kLimit = LOST ? kTestWaitNs : kTensorWaitNs;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Bars bars;
     volatile int *failed = &bars.failed;
@@ -254,8 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tile = (int)(unit / n_cols), col = (int)(unit % n_cols);
                 for (int s = 0; s < n_steps; ++s, copy.step(1, n_ring)) {
                     const uint32_t slot = copy.at;
-                    if (copy.turn > 0) ok = ok && wait(&bars.empty[slot], (copy.turn - 1) & 1, failed);
-                    if (!ok) continue;
+                    if (copy.turn > 0) ok = ok && wait(&bars.empty[slot], (copy.turn - 1) & 1, failed, kLimit);
+                    if (!ok || (LOST && blockIdx.x == 0 && copy.turn > 0)) continue;
                     const int k0 = (step0 + s) * kStep, w0 = tile * C * kRows + w_off, x0 = col * N + x_off;
                     const uint32_t to = smem_addr(ring + slot * kSlot);
                     // of a pair the first block counts both blocks' bytes
@@ -282,8 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < n_steps; ++s, copy.step(1, n_ring)) {
                 const bool begins = EXACT ? s % kExact == 0 : s == 0;
                 const bool ends = s == n_steps - 1 || (EXACT && s % kExact == kExact - 1);
-                if (begins && sums.turn > 0) ok = ok && wait(&bars.taken[sums.at], (sums.turn - 1) & 1, failed);
-                ok = ok && wait(&bars.full[copy.at], copy.turn & 1, failed);
+                if (begins && sums.turn > 0) ok = ok && wait(&bars.taken[sums.at], (sums.turn - 1) & 1, failed, kLimit);
+                ok = ok && wait(&bars.full[copy.at], copy.turn & 1, failed, kLimit);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 tc_after();
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sums.step(1, 2);
         };
         auto made = [&] {
-            ok = ok && wait(&bars.made[sums.at], sums.turn & 1, failed);
+            ok = ok && wait(&bars.made[sums.at], sums.turn & 1, failed, kLimit);
             ok = __all_sync(0xffffffffu, ok);
             tc_after();
         };
@@ -462,14 +465,14 @@ int64_t units_of(const LinearParams &p, int N, int C) {
     return ((int64_t)p.lin.N + C * kRows - 1) / (C * kRows) * (((int64_t)p.n_rows + N - 1) / N);
 }
 
-template <int N, int C, bool SPLIT, bool EXACT>
+template <int N, int C, bool SPLIT, bool EXACT, bool LOST>
 cudaError_t launch(const LinearParams &p, int split, int sms, cudaStream_t stream) {
     constexpr int kSlot = kBytesW + N / C * kStep * 2;
     const int fixed = 1024 + (SPLIT ? (split - 1) * N * kRows * 4 : 0);
     const int n_ring = std::min((kSmem - (int)sizeof(Bars) - fixed) / kSlot, kMostRing);
     // First of all: in a thread that has used no CUDA before, this makes the device's
     // context current, without which the driver refuses to make a map.
-    cudaError_t e = cudaFuncSetAttribute(linear_kernel<N, C, SPLIT, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem - (int)sizeof(Bars));
+    cudaError_t e = cudaFuncSetAttribute(linear_kernel<N, C, SPLIT, EXACT, LOST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem - (int)sizeof(Bars));
     if (e != cudaSuccess) return e;
     CUtensorMap map_w, map_x;
     e = map_of(&map_w, p.lin.w, p.lin.N, p.lin.K, p.lin.w_ld, kRows);
@@ -487,7 +490,7 @@ cudaError_t launch(const LinearParams &p, int split, int sms, cudaStream_t strea
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_kernel<N, C, SPLIT, EXACT>, p, n_ring, map_w, map_x);
+    return cudaLaunchKernelEx(&cfg, linear_kernel<N, C, SPLIT, EXACT, LOST>, p, n_ring, map_w, map_x);
 }
 
 // Blocks that divide k: as many as the multiprocessors have room for, with at least two
@@ -501,34 +504,35 @@ int split_of(const LinearParams &p, int N, int sms) {
     return s;
 }
 
-template <int N>
+template <int N, bool LOST>
 cudaError_t launch_n(const LinearParams &p, int sms, cudaStream_t stream) {
     const bool exact = p.dtype == PS_F32;
     if constexpr (N <= 64) {
         int s = split_of(p, N, sms);
         if (N == 64) s = std::min(s, 4);                       // the first block holds the others' sums
-        if (s > 1) return launch<N, 1, true, true>(p, s, sms, stream);
+        if (s > 1) return launch<N, 1, true, true, LOST>(p, s, sms, stream);
     }
     // One block a tile and two, in us with a cold L2: 64 rows of 262144 x 2048 187 / 191, 128 of
     // 151936 x 4096 218 / 216, 256 of it 275 / 236, 2000 of it 1485 / 1404, 256 of 20000 x 4096
     // 81 / 68; so pairs for 256 rows a tile, where there are tiles for all.
     if constexpr (N == 256)
         if (units_of(p, N, 2) >= sms / 2)
-            return exact ? launch<N, 2, false, true>(p, 1, sms, stream) : launch<N, 2, false, false>(p, 1, sms, stream);
-    return exact ? launch<N, 1, false, true>(p, 1, sms, stream) : launch<N, 1, false, false>(p, 1, sms, stream);
+            return exact ? launch<N, 2, false, true, LOST>(p, 1, sms, stream) : launch<N, 2, false, false, LOST>(p, 1, sms, stream);
+    return exact ? launch<N, 1, false, true, LOST>(p, 1, sms, stream) : launch<N, 1, false, false, LOST>(p, 1, sms, stream);
 }
 
-cudaError_t launch_rows(const LinearParams &p, int sms, cudaStream_t stream) {
-    if (p.n_rows <= 16) return launch_n<16>(p, sms, stream);
-    if (p.n_rows <= 32) return launch_n<32>(p, sms, stream);
-    if (p.n_rows <= 64) return launch_n<64>(p, sms, stream);
-    if (p.n_rows <= 128) return launch_n<128>(p, sms, stream);
-    return launch_n<256>(p, sms, stream);
+cudaError_t launch_rows(const LinearParams &p, int sms, bool lost, cudaStream_t stream) {
+    if (lost) return p.n_rows <= 64 ? launch_n<64, true>(p, sms, stream) : launch_n<256, true>(p, sms, stream);
+    if (p.n_rows <= 16) return launch_n<16, false>(p, sms, stream);
+    if (p.n_rows <= 32) return launch_n<32, false>(p, sms, stream);
+    if (p.n_rows <= 64) return launch_n<64, false>(p, sms, stream);
+    if (p.n_rows <= 128) return launch_n<128, false>(p, sms, stream);
+    return launch_n<256, false>(p, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearParams &params, int sms, cudaStream_t stream) {
+cudaError_t launch_linear(const LinearParams &params, int sms, bool lost, cudaStream_t stream) {
     // The kernel counts rows, a tile's last ones among them, in 32 bits.
     constexpr int64_t kMostRows = (int64_t)1 << 30;             // of a launch
     const int64_t esz = params.dtype == PS_BF16 ? 2 : 4;
@@ -538,7 +542,7 @@ cudaError_t launch_linear(const LinearParams &params, int sms, cudaStream_t stre
         p.x = (const uint8_t *)params.x + r * params.x_ld * 2;
         p.out = (uint8_t *)params.out + r * params.ld * esz;
         if (params.residual) p.residual = (const uint8_t *)params.residual + r * params.residual_ld * esz;
-        const cudaError_t e = launch_rows(p, sms, stream);
+        const cudaError_t e = launch_rows(p, sms, lost, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

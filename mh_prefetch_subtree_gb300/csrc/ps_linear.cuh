@@ -17,6 +17,7 @@ struct LinearParams {
     int64_t ld;
 };
 
-cudaError_t launch_linear(const LinearParams &p, int sms, cudaStream_t stream);
+// lost: ps_selftest_linear_wait.
+cudaError_t launch_linear(const LinearParams &p, int sms, bool lost, cudaStream_t stream);
 
 }  // namespace ps
