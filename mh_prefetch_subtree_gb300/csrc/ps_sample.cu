@@ -24,8 +24,7 @@
 // a bin of several values (float32 rows, values around zero) adds weights of 28 bits below
 // its largest value's: up to 2^-27 of an element at the lower end of a bin that is two units of y
 // wide, the widest.  A token differs from that of a float64 evaluation only where u Z lies that
-// close to a border between two ids.  Such a bin's mass and its elements', each rounded by
-// itself, are two roundings of one sum; what ends with the bin ends where its mass does.
+// close to a border between two ids; equal ids are divided exactly.
 //
 // A row is one block's, or with few rows a cluster's: its blocks each read a part, and the
 // first adds up their bins.
@@ -250,12 +249,6 @@ __device__ __forceinline__ void exponent(float l, float ref, const Scale &s, flo
     *yh = d * s.gh;
     *yl = fmaf(d, s.gh, -*yh) + fmaf(d, s.gl, e * s.gh);
 }
-__device__ __forceinline__ uint64_t mass_of(float l, const Scale &s, const uint64_t *table) {
-    if (!(l >= s.lo)) return 0;
-    float h, e;
-    exponent(l, s.M, s, &h, &e);
-    return h <= -kWindow - 1.f ? 0 : pow2_fixed(h, e, s.bits, table);
-}
 // The reference of the bin of a code that holds several values, where b is one of them or the
 // bin's largest: the largest value itself.
 __device__ __forceinline__ float bin_ref(float l, const Scale &s) {
@@ -270,6 +263,24 @@ __device__ __forceinline__ float bin_ref(float l, const Scale &s) {
 __device__ __forceinline__ uint32_t limbs(float l, float ref, const Scale &s, const uint64_t *table) {
     const float d = l - ref, h = d * s.gh;
     return min((uint32_t)pow2_fixed(h, fmaf(d, s.gh, -h) + d * s.gl, 28, table), (1u << 28) - 1);
+}
+
+// The mass of a value: of one that has a bin of its own w, of the others the share of their
+// bin's mass that their weight is, rounded up.  No bin has more mass than its elements, and equal
+// elements have equal shares of theirs, so that a cut or a number which divides them by a
+// whole number (half of two) finds that number of them.
+template <bool HALF>
+__device__ __forceinline__ uint64_t mass_of(float l, const Scale &s, const uint64_t *table) {
+    if (!(l >= s.lo)) return 0;
+    const bool one = HALF && (int32_t)((__float_as_uint(l) & 0x7fffffffu) >> 16) > s.zero;
+    const float ref = one ? l : bin_ref(l, s);
+    float h, e;
+    exponent(ref, s.M, s, &h, &e);
+    if (!(h > -(float)s.bits - 2.f)) return 0;
+    const uint64_t w = pow2_fixed(h, e, s.bits, table);
+    if (one) return w;
+    const uint64_t m = limbs(l, ref, s, table), low = w * m;
+    return (__umul64hi(w, m) << 36 | low >> 28) + ((low & ((1u << 28) - 1)) != 0);
 }
 
 // ln(m 2^-scale), m > 0, to about 2^-30: an estimate x and how far m e^-x is from 1.
@@ -690,7 +701,7 @@ struct Row {
                 if (k >= c.klo && k <= c.khi && (c.below < 0 || id0 + j * kPer + i < c.below)) {
                     ++n;
                     least = min(least, k), most = max(most, k);
-                    m += mass_of(l, s, sh.pow);
+                    m += mass_of<kHalf>(l, s, sh.pow);
                 }
             }
         });
@@ -1058,12 +1069,11 @@ struct Order : Row<ElemT, ENT> {
     }
     // Of r.equal elements of r.key the cth, or the one where the mass reaches t.
     __device__ __forceinline__ void nth_of(Result &r, uint32_t c, uint64_t t, uint64_t bin_end, uint32_t last) const {
-        const uint64_t w = mass_of(of_key(r.key), s, sh.pow);
+        const uint64_t w = mass_of<kHalf>(of_key(r.key), s, sh.pow);
         const uint32_t left = r.equal;
         uint32_t j = c;
         if (c == 0) {
-            // without a mass (see settle()) the last
-            j = w ? (uint32_t)fminf(__fdividef((float)t, (float)w), (float)left) : left;
+            j = (uint32_t)fminf(__fdividef((float)t, (float)w), (float)left);
             j = max(min(j, left), 1u);
             while (j > 1 && (j - 1) * w >= t) --j;
             while (j < left && j * w < t) ++j;
@@ -1072,8 +1082,8 @@ struct Order : Row<ElemT, ENT> {
         r.nth = j;
         r.before += (j - 1) * w;
         r.count += j - 1;
-        // a bin's mass and those of its elements may differ in their last bits: its last element
-        // ends where the bin does, and none ends later
+        // the elements of a bin of several values are rounded up: its last one ends where the bin
+        // does, and none ends later
         r.end = r.count == last ? bin_end : min(r.before + w, bin_end);
     }
     // The same in a bin of several values: halved until its elements fit the list, or are equal.
@@ -1123,27 +1133,22 @@ struct Order : Row<ElemT, ENT> {
         uint64_t w = 0;
         if (threadIdx.x < len) {
             me = sh.list[threadIdx.x];
-            w = mass_of(of_key(me.x), s, sh.pow);
+            w = mass_of<kHalf>(of_key(me.x), s, sh.pow);
             sh.list_w[threadIdx.x] = w;
         }
         __syncthreads();
         if (threadIdx.x < len) {
-            uint64_t b = 0, all = 0;
+            uint64_t b = 0;
             uint32_t nb = 0, nth = 1, equal = 0;
 #pragma unroll 4
             for (uint32_t i = 0; i < len; ++i) {
                 const uint2 x = sh.list[i];
                 const uint64_t xw = sh.list_w[i];
-                all += xw;
                 const bool same = x.x == me.x && x.y < me.y;
                 if (x.x > me.x || same) b += xw, ++nb;
                 nth += same, equal += x.x == me.x;
             }
-            // t may be more than the elements' masses, each rounded by itself, add up to.  Where all
-            // of them round to none, the bin has its mass at its last element, as the prefix that
-            // ends with the bin is then the first to hold t.
-            const uint64_t to = min(t, all);
-            if (number ? nb + 1 == c : all == 0 ? nb + 1 == len : b < to && b + w >= to) {
+            if (number ? nb + 1 == c : b < t && b + w >= t) {
                 Result q;
                 q.before = r.before + b;
                 q.count = r.count + nb;
@@ -1407,7 +1412,7 @@ __global__ void __launch_bounds__(Row<ElemT, ENT>::kT, Row<ElemT, ENT>::kResiden
     if (tid == kT - 1 && p.lq) {
         double lq = -(double)kInf;
         if (kept) {
-            const uint64_t w = mass_of(l, s, sh.pow);
+            const uint64_t w = mass_of<kHalf>(l, s, sh.pow);
             if (2 * w > Z) {                                     // a mass close to all of Z: by the others' share
                 lq = -(double)log1pf((float)(Z - min(w, Z)) / (float)w);
             } else {
