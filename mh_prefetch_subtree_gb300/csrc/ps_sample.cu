@@ -726,7 +726,8 @@ struct Row {
     }
     __device__ void gather(const Command &c) {
         const uint32_t n_at = at_block(&sh.n_list, 0), at = at_block(&sh.list[0], 0);
-        const float least = of_key(c.klo), most = of_key(c.khi);
+        // the key below 0's is no value's, and as a float, -0, would stand for 0
+        const float least = of_key(c.klo), most = of_key(c.khi - (c.khi == 0x7fffffffu));
         each([&](const uint4 &v, int j) {
             float x[kPer];
             floats(v, x);
