@@ -265,22 +265,27 @@ __device__ __forceinline__ uint32_t limbs(float l, float ref, const Scale &s, co
     return min((uint32_t)pow2_fixed(h, fmaf(d, s.gh, -h) + d * s.gl, 28, table), (1u << 28) - 1);
 }
 
-// The mass of a value: of one that has a bin of its own w, of the others the share of their
-// bin's mass that their weight is, rounded up.  No bin has more mass than its elements, and equal
-// elements have equal shares of theirs, so that a cut or a number which divides them by a
-// whole number (half of two) finds that number of them.
+// w, as a mass.
+__device__ __forceinline__ uint64_t mass_at(float l, const Scale &s, const uint64_t *table) {
+    float h, e;
+    exponent(l, s.M, s, &h, &e);
+    return h > -(float)s.bits - 2.f ? pow2_fixed(h, e, s.bits, table) : 0;
+}
+// The mass of an element of a bin of several values, whose reference has the mass w: the share of it that
+// the element's weight is, rounded up.  So no bin has more mass than its elements, and equal
+// elements have equal shares of theirs: a cut or a number which divides them by a whole
+// number (half of two) finds that number of them.
+__device__ __forceinline__ uint64_t mass_in(float l, float ref, uint64_t w, const Scale &s, const uint64_t *table) {
+    const uint64_t m = limbs(l, ref, s, table), low = w * m;
+    return (__umul64hi(w, m) << 36 | low >> 28) + ((low & ((1u << 28) - 1)) != 0);
+}
 template <bool HALF>
 __device__ __forceinline__ uint64_t mass_of(float l, const Scale &s, const uint64_t *table) {
     if (!(l >= s.lo)) return 0;
     const bool one = HALF && (int32_t)((__float_as_uint(l) & 0x7fffffffu) >> 16) > s.zero;
     const float ref = one ? l : bin_ref(l, s);
-    float h, e;
-    exponent(ref, s.M, s, &h, &e);
-    if (!(h > -(float)s.bits - 2.f)) return 0;
-    const uint64_t w = pow2_fixed(h, e, s.bits, table);
-    if (one) return w;
-    const uint64_t m = limbs(l, ref, s, table), low = w * m;
-    return (__umul64hi(w, m) << 36 | low >> 28) + ((low & ((1u << 28) - 1)) != 0);
+    const uint64_t w = mass_at(ref, s, table);
+    return one ? w : mass_in(l, ref, w, s, table);
 }
 
 // ln(m 2^-scale), m > 0, to about 2^-30: an estimate x and how far m e^-x is from 1.
@@ -688,6 +693,9 @@ struct Row {
 
     __device__ void count(const Command &c) {
         uint32_t n = 0, least = 0xffffffffu, most = 0;
+        // masses are asked for within a bin of several values
+        const float ref = bin_ref(of_key(c.khi), s);
+        const uint64_t w = mass_at(ref, s, sh.pow);
         uint64_t m = 0;
         each([&](const uint4 &v, int j) {
             float x[kPer];
@@ -701,7 +709,7 @@ struct Row {
                 if (k >= c.klo && k <= c.khi && (c.below < 0 || id0 + j * kPer + i < c.below)) {
                     ++n;
                     least = min(least, k), most = max(most, k);
-                    m += mass_of<kHalf>(l, s, sh.pow);
+                    m += mass_in(l, ref, w, s, sh.pow);
                 }
             }
         });
