@@ -676,7 +676,9 @@ ps_status ps_selftest_head_wait(const ps_head *head, const void *hidden, int64_t
  * (ps_process_rows) come first: the rows given here are the processed ones.
  *
  * Masses are integers of 2^-43 or finer, so that results do not depend on the order of
- * sums; a log q between -1e-12 and 0 may come as 0.
+ * sums; a log q between -1e-12 and 0 may come as 0.  A cut or a token may differ from the
+ * exact sums' by a neighbour where a border lies within 2^-27 of the running mass (2^-31 in
+ * bfloat16 rows), and 2^-43 for each id; equal largest ids are divided exactly.
  */
 typedef struct {
     int64_t n_sets;

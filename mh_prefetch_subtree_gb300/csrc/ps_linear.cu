@@ -7,10 +7,10 @@
 // out (four took as long as the products: 2000 rows 2411 us); sums have two places, so that
 // one tile's leave while the next one's are made.
 //   N   16, 32, 64, 128 or 256: what the rows of x fill.  Few rows are bound by the weights'
-//       bytes, for which the ring holds 200 KB under way: one row of 151936 x 4096 takes 188
-//       us, 6.6 TB/s.  Many are bound by the products: 2000 rows 1582 us, 1.57 PFLOP/s;
-//       small K by the way out: 1158 rows of 262144 x 256 222 us (450 before outputs were
-//       converted in pairs and their addresses stepped).
+//       bytes, for which the ring holds 200 KB under way: one row of 151936 x 4096 takes 184
+//       to 189 us, 6.6 TB/s.  Many are bound by the products: 2000 rows 1560 us, 1.6 PFLOP/s;
+//       small K by the way out: 1158 rows of 262144 x 256 222 to 257 us (450 before outputs
+//       were converted in pairs and their addresses stepped), capped 384 to 457.
 //   C   of 256 rows a tile two blocks share a product and bring half of x's rows each.
 //   S   where W has too few tiles for all multiprocessors and few rows of x, the S blocks of
 //       a cluster divide k, and the first adds the others' float32 sums in their order.

@@ -24,17 +24,20 @@
 // a bin of several values (float32 rows, values around zero) adds weights of 28 bits below
 // its largest value's: up to 2^-27 of an element at the lower end of a bin that is two units of y
 // wide, the widest.  A token differs from that of a float64 evaluation only where u Z lies that
-// close to a border between two ids; equal ids are divided exactly.
+// close to a border between two ids, or to the 2^-43 or so by which each id's mass is rounded;
+// a cut or a number that divides equal largest ids by a whole number finds that number of them.
 //
 // A row is one block's, or with few rows a cluster's: its blocks each read a part, and the
 // first adds up their bins.
 //
-// What bounds it, for many rows: the additions in shared memory.  A warp's 32 go to random
-// banks, which takes four turns, so a bfloat16 row of 151936 is 19 thousand turns of the 35
-// thousand cycles that it takes of a multiprocessor (4,000 of them scored: 440 us, 2.8 TB/s;
-// issue slots 54% busy).  float32 rows need three additions an element and two or three more
-// readings (777 x 50021: 196 us).  For few rows: the chain of small steps after the pass,
-// about 12 us of the 25 that 16 rows of 151936 take.  Measured and not kept: the row held in
+// What bounds it: no unit is full.  A warp's 32 additions go to random banks, which takes four
+// turns of shared memory.  Of many bfloat16 rows scored these turns are 58% of the cycles, and
+// issue slots 54% (4,000 x 151936: 440 to 460 us, 2.7 TB/s); drawn, with a second reading, 49% and 45%
+// (700 x 262144: 187 us).  The rest are passes and chains of small steps that do not overlap.
+// float32 rows take three additions an element, a weight for each and two or three more
+// readings: turns 29%, issue slots 60% (777 x 50021: 194 us; 1216 x 151936: 795 us, drawn 935).
+// For few rows: the chain of small steps after the pass, about 12 us of the 25 that 16 rows of
+// 151936 take.  Measured and not kept: the row held in
 // the shared memory of a cluster, with the maximum found first (4,000 rows 1,197 us); logits
 // more than 10 tau below the largest summed by exponentials and not counted (445 to 540);
 // copies through a ring in shared memory (500); one 64-bit addition for a float32 element's
