@@ -441,13 +441,27 @@ cudaError_t launch_u(const HeadParams &p, int sms, cudaStream_t stream) {
                                          : launch_n<U, float>(p, sms, stream);
 }
 
-}  // namespace
-
-cudaError_t launch_head_rows(const HeadParams &p, int sms, cudaStream_t stream) {
+cudaError_t launch_some(const HeadParams &p, int sms, cudaStream_t stream) {
     if (head_tile_takes(p, sms)) return launch_head_tile(p, sms, stream);
     if (p.head.group == 32) return launch_u<32>(p, sms, stream);
     if (p.head.group == 64) return launch_u<64>(p, sms, stream);
     return launch_u<128>(p, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_head_rows(const HeadParams &params, int sms, cudaStream_t stream) {
+    // The kernels count rows, a tile's last ones among them, in 32 bits.
+    constexpr int64_t kMostRows = (int64_t)1 << 30;             // of a launch
+    for (int64_t r = 0; r < params.n_rows; r += kMostRows) {
+        HeadParams p = params;
+        p.n_rows = (int32_t)(params.n_rows - r < kMostRows ? params.n_rows - r : kMostRows);
+        p.hidden = params.hidden + r * params.hidden_ld;
+        p.logits = (uint8_t *)params.logits + r * params.ld * (params.dtype == PS_BF16 ? 2 : 4);
+        const cudaError_t e = launch_some(p, sms, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace ps
