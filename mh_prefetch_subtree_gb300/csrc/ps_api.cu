@@ -146,7 +146,7 @@ using namespace ps;
 
 extern "C" {
 
-const char *ps_version(void) { return "libps 0.6.0 (sm_103a)"; }
+const char *ps_version(void) { return "libps 0.6.1 (sm_103a)"; }
 
 const char *ps_status_string(ps_status s) {
     switch (s) {
